@@ -260,6 +260,70 @@ MOE_API int moe_routing_map_to_topk(const moe_problem *p, const uint8_t *routing
                                                   workspace, static_cast<hipStream_t>(stream)));
 }
 
+MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan, const uint16_t *expert_out,
+                                 const float *topk_weights, const uint16_t *dout, uint16_t *dy,
+                                 float *dweights, void *stream) {
+  const int rc = check_combine_backward_args(p, plan, expert_out, topk_weights, dout, dy, dweights);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_combine_backward(*p, *plan, expert_out, topk_weights, dout, dy, dweights,
+                                               static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_check_expert_op(const moe_problem *p, const moe_expert_op *op) {
+  return check_expert_op(p, op);
+}
+
+MOE_API size_t moe_expert_workspace_bytes(const moe_problem *p, const moe_expert_op *op) {
+  if (check_expert_op(p, op) != MOE_OK) return 0;
+  return moe::expert_workspace_bytes(*p, *op);
+}
+
+MOE_API int moe_expert_glu(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                           const void *x, const float *x_scales, const void *w, const float *w_scales,
+                           const float *bias, uint16_t *h, uint16_t *preact, void *stream) {
+  const int rc = check_expert_forward_args(p, plan, op, x, x_scales, w, w_scales, bias, nullptr, h, preact);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_expert_forward(*p, *plan, *op, true,
+                                             {x, w, x_scales, w_scales, bias, nullptr, h, preact},
+                                             static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_expert_linear(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                              const void *x, const float *x_scales, const void *w, const float *w_scales,
+                              const float *bias, const uint16_t *residual, uint16_t *y, uint16_t *preact,
+                              void *stream) {
+  const int rc =
+      check_expert_forward_args(p, plan, op, x, x_scales, w, w_scales, bias, residual, y, preact);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_expert_forward(*p, *plan, *op, false,
+                                             {x, w, x_scales, w_scales, bias, residual, y, preact},
+                                             static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_expert_glu_backward(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                                    const uint16_t *dh, const uint16_t *preact, const uint16_t *x,
+                                    const uint16_t *w, uint16_t *dz, uint16_t *dx, uint16_t *dw,
+                                    float *dbias, void *workspace, void *stream) {
+  const int rc =
+      check_expert_backward_args(p, plan, op, true, dh, preact, x, w, dz, dx, dw, dbias, workspace);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_expert_backward(*p, *plan, *op, true,
+                                              {dh, preact, x, w, dz, dx, dw, dbias, workspace},
+                                              static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_expert_linear_backward(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                                       const uint16_t *dy, const uint16_t *preact, const uint16_t *x,
+                                       const uint16_t *w, uint16_t *dz, uint16_t *dx, uint16_t *dw,
+                                       float *dbias, void *workspace, void *stream) {
+  const int rc =
+      check_expert_backward_args(p, plan, op, false, dy, preact, x, w, dz, dx, dw, dbias, workspace);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_expert_backward(*p, *plan, *op, false,
+                                              {dy, preact, x, w, dz, dx, dw, dbias, workspace},
+                                              static_cast<hipStream_t>(stream)));
+}
+
 MOE_API const char *moe_strerror(int code) { return error_text(code); }
 
 }  // extern "C"

@@ -1,0 +1,425 @@
+// expert_tile.hpp -- the matrix-product engine of the experts' kernels
+// (gfx950 MFMA): one workgroup computes a BI x BJ tile of
+//
+//   O[i][j] = sum_c I(i, c) * J(j, c),
+//
+// j contiguous in memory.  An operand is stored either "along c" (its rows
+// are i or j, the contraction index is contiguous: token rows and weights of
+// the forward products) or "across c" (its rows are the contraction index:
+// the weights in the rows' gradient, both operands of the weights' gradient).
+//
+// J is the MFMA's A operand and I its B operand, so that a lane ends with four
+// neighbouring j of one i: 8-byte stores of bf16, and one row scale per lane.
+//
+// Memory path.  A step covers 128 bytes of the contraction (64 bf16 or 128
+// E4M3 values).  Tiles go from global memory straight into LDS (16 bytes a
+// lane, no registers), NST stages deep: the loads of step t + NST - 1 are
+// issued before the products of step t, and one barrier a step both publishes
+// a stage and frees the one before it.  Such a load writes 64 consecutive 16-byte chunks of
+// LDS, so there is no padding against bank conflicts; instead a lane picks which
+// chunk of its row it fetches:
+//   along c:  rows of 8 chunks, chunk c of row r at position c ^ (r & 7); the
+//             16-byte operand reads of 8 consecutive lanes (8 rows, one chunk
+//             index) then touch 8 different positions;
+//   across c: rows of 16-column groups (32 bytes), group g of row r at
+//             g ^ f(r), f taking r's bits 0, 1, 3, 4: the 16 rows that one
+//             transposing read visits for one group then lie in different banks.
+// Rows, columns and contraction indices past an operand's end are loads past
+// the buffer resource: they fetch nothing and leave zeros in LDS.
+#pragma once
+
+#include <type_traits>
+
+#include "moe_device.hpp"
+#include "moe_kernels.hpp"
+
+namespace moe {
+namespace tile {
+
+#define MOE_LDS __attribute__((address_space(3)))
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef MOE_LDS char *lds_ptr;
+
+constexpr int kStepBytes = 128;  // contraction bytes of one step
+constexpr int kStepRows = 64;    // contraction rows of one step, stored across c
+// An offset past every buffer resource used here (their size is 2^31 - 1).
+constexpr uint32_t kNowhere = 0x80000000u;
+constexpr uint32_t kRecords = 0x7FFFFFFFu;
+
+// WI x WJ waves; each owns FI x FJ blocks of 16 x 16.  XI/XJ: the operand is
+// stored across c.  FP8: E4M3 codes (along c only) with block scales.
+template <int BI_, int BJ_, int WI_, int WJ_, int NST_, bool XI_ = false, bool XJ_ = false,
+          bool FP8_ = false>
+struct Shape {
+  static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_;
+  static constexpr bool XI = XI_, XJ = XJ_, FP8 = FP8_;
+  static constexpr int kThreads = WI * WJ * kWave;
+  // at least two waves a SIMD: that also keeps the accumulators in the 256
+  // registers that both operands and results of an MFMA can name (with more, the
+  // compiler moves them to and from the accumulation registers in the loop)
+  static constexpr int kWavesPerSimd = 2;
+  static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
+  // 16-byte loads a thread makes for an operand in a step; a tile smaller than one load
+  // of every thread still gets a whole one (its spare rows are zeros)
+  static constexpr int loads(int b) { return (b * 8 + kThreads - 1) / kThreads; }
+  static constexpr int LI = loads(BI), LJ = loads(BJ);
+  static constexpr int kBytesI = LI * kThreads * 16, kBytesJ = LJ * kThreads * 16;
+  static constexpr int kBytesScale = FP8 ? kThreads * 4 : 0;  // of each operand
+  static constexpr int kStage = kBytesI + kBytesJ + 2 * kBytesScale;
+  static constexpr int kLdsBytes = NST * kStage;
+  static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // in flight per stage and wave
+  static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
+  static_assert(kLoads * (NST - 2) < 64, "the wait counter holds 63 loads");
+  static_assert(kLdsBytes <= 160 * 1024, "LDS of a compute unit");
+};
+
+// -------------------------------------------------------------- loaders ---
+
+__device__ __forceinline__ int wave_id() {
+  return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+}
+
+__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, lds_ptr to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, static_cast<int>(off), 0, 0, 0);
+}
+
+// Rows stored along c.  row_offset(r): byte offset from `base` of tile row r,
+// or kNowhere; row_bytes: bytes of a whole row (a multiple of 16).
+template <class S, int L>
+struct AlongLoader {
+  const char *base;
+  int row_bytes;
+  int chunk;         // byte offset in a step of the chunk this lane fetches
+  uint32_t off[L];
+
+  template <class F>
+  __device__ __forceinline__ void init(const void *b, int bytes, F row_offset) {
+    base = static_cast<const char *>(b);
+    row_bytes = bytes;
+    const int tid = threadIdx.x;
+    chunk = ((tid & 7) ^ ((tid >> 3) & 7)) * 16;
+#pragma unroll
+    for (int u = 0; u < L; ++u) {
+      const uint32_t o = row_offset((u * S::kThreads + tid) >> 3);
+      off[u] = o == kNowhere ? kNowhere : o + chunk;
+    }
+  }
+  __device__ __forceinline__ void issue(lds_ptr to, int step) const {
+    const int at = step * kStepBytes;
+    const auto r = buffer_rsrc(base + at, kRecords);
+    const bool ok = at + chunk < row_bytes;
+    const int wave = wave_id();
+#pragma unroll
+    for (int u = 0; u < L; ++u)
+      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16, ok ? off[u] : kNowhere);
+  }
+};
+
+// The bank-spreading term of contraction row r in a tile of G 16-column groups.
+template <int G>
+__device__ __forceinline__ int group_mix(int r) {
+  return ((r & 3) | (((r >> 3) & 3) << 2)) & (G - 1);
+}
+
+// Rows stored across c: `rows` contraction rows of `ld` bytes; B columns from
+// `base`, of which `cols` exist.
+template <class S, int B, int L>
+struct AcrossLoader {
+  static constexpr int kChunks = B / 8;                 // 16-byte chunks of a tile row
+  static constexpr int kRowStep = S::kThreads / kChunks;  // rows between a thread's loads
+  static_assert(kStepRows * kChunks % S::kThreads == 0, "whole loads");
+  const char *base;
+  int64_t ld;
+  int rows;
+  uint32_t off[L];
+
+  __device__ __forceinline__ void init(const void *b, int64_t row_bytes, int nrows, int cols) {
+    base = static_cast<const char *>(b);
+    ld = row_bytes;
+    rows = nrows;
+    const int ch = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+#pragma unroll
+    for (int u = 0; u < L; ++u) {
+      const int r = u * kRowStep + r0;
+      const int col = ((ch >> 1) ^ group_mix<B / 16>(r)) * 16 + (ch & 1) * 8;
+      off[u] = col < cols ? static_cast<uint32_t>(r * static_cast<int>(ld) + col * 2) : kNowhere;
+    }
+  }
+  __device__ __forceinline__ void issue(lds_ptr to, int step) const {
+    const auto r = buffer_rsrc(base + step * kStepRows * ld, kRecords);
+    const int left = rows - step * kStepRows - static_cast<int>(threadIdx.x) / kChunks;
+    const int wave = wave_id();
+#pragma unroll
+    for (int u = 0; u < L; ++u)
+      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16,
+                 u * kRowStep < left ? off[u] : kNowhere);
+  }
+};
+
+// Block scales of an FP8 step: thread r fetches the scale of tile row r, and
+// that of the weights' block r of the tile.
+struct ScaleLoader {
+  const float *rows, *weights;
+  uint32_t row_off, weight_off;  // bytes, of step 0
+  template <class S>
+  __device__ __forceinline__ void issue(lds_ptr to, int step, int steps) const {
+    const bool ok = step < steps;
+    to += wave_id() * kWave * 4;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(rows + step, kRecords), (MOE_LDS void *)to, 4,
+                                             static_cast<int>(ok ? row_off : kNowhere), 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(weights + step, kRecords),
+                                             (MOE_LDS void *)(to + S::kBytesScale), 4,
+                                             static_cast<int>(ok ? weight_off : kNowhere), 0, 0, 0);
+  }
+};
+struct NoScales {};
+
+// ------------------------------------------------------------- operands ---
+
+// Where a lane finds its part of an operand's 16-row blocks in a stage.
+template <int F, int B, bool X>
+struct Fragments;
+
+template <int F, int B>
+struct Fragments<F, B, false> {
+  int at[2];  // contraction halves of the step
+  __device__ __forceinline__ void init(int first_block) {
+    const int l = lane_id();
+    at[0] = first_block * 16 * kStepBytes + (l & 15) * kStepBytes + (((l >> 4) ^ (l & 7)) * 16);
+    at[1] = at[0] ^ 64;
+  }
+  __device__ __forceinline__ i32x4 read(lds_ptr t, int b, int half) const {
+    return *(MOE_LDS const i32x4 *)(t + at[half] + b * 16 * kStepBytes);
+  }
+};
+
+template <int F, int B>
+struct Fragments<F, B, true> {
+  int at[F];
+  __device__ __forceinline__ void init(int first_block) {
+    const int l = lane_id(), q = l >> 4, r = q * 8 + ((l >> 2) & 3);
+#pragma unroll
+    for (int b = 0; b < F; ++b)
+      at[b] = r * B * 2 + ((first_block + b) ^ group_mix<B / 16>(r)) * 32 + (l & 3) * 8;
+  }
+  // two transposing reads: contraction rows 8q .. 8q+3 and 8q+4 .. 8q+7 of the half
+  __device__ __forceinline__ i32x4 read(lds_ptr t, int b, int half) const {
+    typedef int i32x2 __attribute__((ext_vector_type(2)));
+    lds_ptr p = t + at[b] + half * 32 * B * 2;
+    const i32x2 lo = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)p));
+    const i32x2 hi = __builtin_bit_cast(
+        i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((MOE_LDS s16x4 *)(p + 4 * B * 2)));
+    return __builtin_shufflevector(lo, hi, 0, 1, 2, 3);
+  }
+};
+
+// ------------------------------------------------------------ main loop ---
+
+template <int N>
+__device__ __forceinline__ void wait_and_meet() {
+  // this wave's loads of the stage have landed and its LDS reads are done;
+  // past the barrier that holds for every wave
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// acc[fi][fj] += the products of `steps` steps.  scale_j(fj): index of the
+// weights' scale of block fj in the stage's scale row (FP8 only).
+template <class S, class LoadI, class LoadJ, class Scales, class ScaleJ>
+__device__ __forceinline__ void multiply(lds_ptr lds, int steps, const LoadI &li, const LoadJ &lj,
+                                         const Scales &sc, ScaleJ scale_j, int wi, int wj,
+                                         f32x4 (&acc)[S::FI][S::FJ]) {
+  Fragments<S::FI, S::BI, S::XI> fi;
+  Fragments<S::FJ, S::BJ, S::XJ> fj;
+  fi.init(wi * S::FI);
+  fj.init(wj * S::FJ);
+#pragma unroll
+  for (int a = 0; a < S::FI; ++a)
+#pragma unroll
+    for (int b = 0; b < S::FJ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+  auto issue = [&](int step, int stage) {
+    lds_ptr to = lds + stage * S::kStage;
+    li.issue(to, step);
+    lj.issue(to + S::kBytesI, step);
+    if constexpr (S::FP8) sc.template issue<S>(to + S::kBytesI + S::kBytesJ, step, steps);
+  };
+#pragma unroll
+  for (int s = 0; s < S::NST - 1; ++s) issue(s, s);
+  int stage = 0;
+  for (int t = 0; t < steps; ++t) {
+    wait_and_meet<S::kLoads *(S::NST - 2)>();
+    // the stage that every wave has just finished reading
+    issue(t + S::NST - 1, stage == 0 ? S::NST - 1 : stage - 1);
+    lds_ptr ti = lds + stage * S::kStage, tj = ti + S::kBytesI;
+    if constexpr (S::FP8) {
+      lds_ptr ts = tj + S::kBytesJ;
+      float si[S::FI], sj[S::FJ];
+#pragma unroll
+      for (int a = 0; a < S::FI; ++a)
+        si[a] = *(MOE_LDS const float *)(ts + ((wi * S::FI + a) * 16 + (lane_id() & 15)) * 4);
+#pragma unroll
+      for (int b = 0; b < S::FJ; ++b) sj[b] = *(MOE_LDS const float *)(ts + S::kBytesScale + scale_j(b) * 4);
+      i32x8 vj[S::FJ];
+#pragma unroll
+      for (int b = 0; b < S::FJ; ++b)
+        vj[b] = __builtin_shufflevector(fj.read(tj, b, 0), fj.read(tj, b, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+      for (int a = 0; a < S::FI; ++a) {
+        const i32x8 vi =
+            __builtin_shufflevector(fi.read(ti, a, 0), fi.read(ti, a, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+#pragma unroll
+        for (int b = 0; b < S::FJ; ++b) {
+          const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              vj[b], vi, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+          const float s = si[a] * sj[b];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[a][b][i] = __builtin_fmaf(d[i], s, acc[a][b][i]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        bf16x8 vi[S::FI], vj[S::FJ];
+#pragma unroll
+        for (int b = 0; b < S::FJ; ++b) vj[b] = __builtin_bit_cast(bf16x8, fj.read(tj, b, half));
+#pragma unroll
+        for (int a = 0; a < S::FI; ++a) vi[a] = __builtin_bit_cast(bf16x8, fi.read(ti, a, half));
+#pragma unroll
+        for (int a = 0; a < S::FI; ++a)
+#pragma unroll
+          for (int b = 0; b < S::FJ; ++b)
+            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vj[b], vi[a], acc[a][b], 0, 0, 0);
+      }
+    }
+    stage = stage + 1 == S::NST ? 0 : stage + 1;
+  }
+  // the last stages' loads fetched nothing, but write LDS: drained before the
+  // workgroup gives it up
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+}
+
+// ---------------------------------------------------------- expert rows ---
+
+// Rows of expert e that hold a token, whatever the plan's arrays hold:
+// start + count stays within `rows`.
+struct ExpertRows {
+  int start, count;
+};
+__device__ __forceinline__ ExpertRows expert_rows(const int32_t *offsets, const int32_t *counts, int e,
+                                                  int rows) {
+  const int a = offsets[e], b = offsets[e + 1];
+  ExpertRows r;
+  r.start = min(max(a, 0), rows);
+  const int64_t room = static_cast<int64_t>(b) - a;  // the fixed capacity may be less than the count
+  int64_t n = counts[e];
+  n = n < room ? n : room;
+  n = n < rows - r.start ? n : rows - r.start;
+  r.count = n > 0 ? static_cast<int>(n) : 0;
+  return r;
+}
+
+struct RowTile {
+  int e;          // expert, -1: no tile for this workgroup
+  int start, count;  // its rows
+  int i0, j;      // first row of the tile in the expert, column tile
+};
+
+// Row tiles are handed out expert by expert, groups of 8 row tiles at a time,
+// every column tile of a group before the next; neighbours in this order share
+// an expert's weights and rows.  Workgroups go round the 8 XCDs in turn, so an
+// XCD takes one contiguous run of the order: its L2 sees each panel once.
+template <int BI>
+__device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, const int32_t *counts,
+                                                 int n_experts, int rows, int col_tiles) {
+  const int lane = lane_id();
+  const int per = (n_experts + kWave - 1) / kWave;  // experts a lane adds up
+  int mine = 0;
+  for (int u = 0; u < per; ++u) {
+    const int e = lane * per + u;
+    if (e < n_experts) mine += (expert_rows(offsets, counts, e, rows).count + BI - 1) / BI;
+  }
+  const int incl = wave_incl_scan(mine);
+  RowTile r;
+  r.e = -1;
+  const int64_t total = static_cast<int64_t>(__builtin_amdgcn_readlane(incl, kWave - 1)) * col_tiles;
+  const int64_t chunk = (total + 7) / 8;
+  const int64_t pos = blockIdx.x / 8, t = (blockIdx.x % 8) * chunk + pos;
+  if (pos >= chunk || t >= total) return r;
+  const uint64_t past = ballot(static_cast<int64_t>(incl) * col_tiles > t);
+  const int owner = __builtin_ctzll(past);
+  int before = __builtin_amdgcn_readlane(incl - mine, owner);
+  // the owner's experts, one per lane (per <= 16)
+  const int e = owner * per + lane;
+  ExpertRows x{0, 0};
+  if (lane < per && e < n_experts) x = expert_rows(offsets, counts, e, rows);
+  const int tiles = (x.count + BI - 1) / BI;
+  const int upto = wave_incl_scan(tiles);
+  const int who = __builtin_ctzll(ballot(static_cast<int64_t>(before + upto) * col_tiles > t));
+  r.e = owner * per + who;
+  r.start = __builtin_amdgcn_readlane(x.start, who);
+  r.count = __builtin_amdgcn_readlane(x.count, who);
+  const int ti = __builtin_amdgcn_readlane(tiles, who);
+  before += __builtin_amdgcn_readlane(upto - tiles, who);
+  const int q = static_cast<int>(t - static_cast<int64_t>(before) * col_tiles);
+  const int group = q / (8 * col_tiles), rest = q - group * 8 * col_tiles;
+  const int size = min(8, ti - group * 8);
+  r.j = rest / size;
+  r.i0 = (group * 8 + rest - r.j * size) * BI;
+  return r;
+}
+
+// Workgroups that cover every row tile of any routing of at most `pairs` rows.
+template <int BI>
+inline int64_t row_tile_bound(int64_t pairs, int n_experts) {
+  const int64_t used = pairs < n_experts ? pairs : n_experts;
+  return (pairs + used * (BI - 1)) / BI;
+}
+
+// ---------------------------------------------------------- activations ---
+
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// value and slope of an activation (a moe_act)
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid(z);
+  if constexpr (ACT == MOE_ACT_GELU_TANH)  // (1 + tanh a) / 2 = sigmoid(2a)
+    return z * sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+  if constexpr (ACT == MOE_ACT_RELU) return z < 0.0f ? 0.0f : z;  // a NaN stays one
+  return z;
+}
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z) {
+  if constexpr (ACT == MOE_ACT_SILU) {
+    const float s = sigmoid(z);
+    return s * (1.0f + z * (1.0f - s));
+  }
+  if constexpr (ACT == MOE_ACT_GELU_TANH) {
+    // sigmoid' has left the fp32 range of 1 long before; z * z could overflow
+    if (fabsf(z) > 16.0f) return z > 0.0f ? 1.0f : 0.0f;
+    const float s = sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+    return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+  }
+  if constexpr (ACT == MOE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  return 1.0f;
+}
+
+// f(integral_constant<ACT>) for a runtime activation
+template <class F>
+inline hipError_t with_act(int act, F f) {
+  switch (act) {
+    case MOE_ACT_SILU: return f(std::integral_constant<int, MOE_ACT_SILU>());
+    case MOE_ACT_GELU_TANH: return f(std::integral_constant<int, MOE_ACT_GELU_TANH>());
+    case MOE_ACT_RELU: return f(std::integral_constant<int, MOE_ACT_RELU>());
+    default: return f(std::integral_constant<int, MOE_ACT_NONE>());
+  }
+}
+
+}  // namespace tile
+}  // namespace moe

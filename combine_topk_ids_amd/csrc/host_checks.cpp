@@ -112,6 +112,11 @@ int64_t expert_capacity(int64_t n_tokens, int32_t top_k, int32_t n_experts, doub
   return static_cast<int64_t>(cap);
 }
 
+size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op) {
+  const size_t chunks = static_cast<size_t>(max_rows(p)) / kBiasChunkRows + p.n_experts + 1;
+  return align256(chunks * 2 * static_cast<size_t>(op.out_dim) * sizeof(float));
+}
+
 namespace host {
 
 int check_problem(const moe_problem *p) {
@@ -349,6 +354,79 @@ int check_map_args(const moe_problem *p, const uint8_t *routing_map, const float
   if (p->n_tokens > 0 && (!routing_map || !topk_ids || !workspace)) return MOE_EINVAL;
   if (!aligned(probs, 4) || !aligned(topk_ids, 4) || !aligned(topk_weights, 4) || !aligned(status, 4) ||
       !aligned(workspace, 256))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_combine_backward_args(const moe_problem *p, const moe_plan *plan, const uint16_t *expert_out,
+                                const float *topk_weights, const uint16_t *dout, const uint16_t *dy,
+                                const float *dweights) {
+  const int rc = check_problem(p);
+  if (rc != MOE_OK) return rc;
+  if (!plan) return MOE_EINVAL;
+  // no gradient of weights that the combine did not take
+  if (dweights && !topk_weights && p->n_tokens > 0) return MOE_EINVAL;
+  if (p->n_tokens > 0 && (!dout || !plan->slot)) return MOE_EINVAL;
+  if (p->n_tokens > 0 && max_rows(*p) > 0 && (!dy || (dweights && !expert_out))) return MOE_EINVAL;
+  if (!aligned(expert_out, 16) || !aligned(dout, 16) || !aligned(dy, 16) || !aligned(topk_weights, 4) ||
+      !aligned(dweights, 4) || !aligned(plan->slot, 4))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_expert_op(const moe_problem *p, const moe_expert_op *op) {
+  const int rc = check_problem(p);
+  if (rc != MOE_OK) return rc;
+  if (!op) return MOE_EINVAL;
+  const int unit = op->fmt == MOE_FMT_BF16 ? 8 : 128;  // a 16-byte row unit, or a scale block
+  if (op->fmt != MOE_FMT_BF16 && op->fmt != MOE_FMT_FP8_E4M3_B128) return MOE_EINVAL;
+  if (op->in_dim <= 0 || op->out_dim <= 0 || op->in_dim % unit || op->out_dim % unit) return MOE_EINVAL;
+  if (op->act < MOE_ACT_NONE || op->act > MOE_ACT_RELU) return MOE_EINVAL;
+  // byte offsets in one expert's weights (up to 2 * out_dim rows of bf16) and
+  // in a tile of 256 rows fit the kernels' 31-bit buffer offsets
+  const int64_t in = op->in_dim, out = op->out_dim;
+  if (in > (1 << 20) || out > (1 << 20) || in * out >= (int64_t{1} << 29)) return MOE_EOVERFLOW;
+  // a launch has one workgroup per tile of at least 64 rows (or one per expert) by 64 columns
+  const int64_t wide = (in > 2 * out ? in : 2 * out) / 64 + 1;
+  if ((expert_row_bound(*p) / 64 + p->n_experts) * wide >= (int64_t{1} << 22)) return MOE_EOVERFLOW;
+  return MOE_OK;
+}
+
+int check_expert_forward_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                              const void *x, const float *x_scales, const void *w, const float *w_scales,
+                              const float *bias, const uint16_t *residual, const uint16_t *y,
+                              const uint16_t *preact) {
+  const int rc = check_expert_op(p, op);
+  if (rc != MOE_OK) return rc;
+  if (!plan || !plan->expert_counts || !plan->expert_offsets) return MOE_EINVAL;
+  const bool fp8 = op->fmt == MOE_FMT_FP8_E4M3_B128;
+  if (!fp8 && (x_scales || w_scales)) return MOE_EINVAL;
+  if (expert_row_bound(*p) > 0 && (!x || !w || !y || (fp8 && (!x_scales || !w_scales)))) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(preact, 16) ||
+      !aligned(residual, 16) || !aligned(bias, 16) || !aligned(x_scales, 4) || !aligned(w_scales, 4) ||
+      !aligned(plan->expert_counts, 4) || !aligned(plan->expert_offsets, 4))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_expert_backward_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                               bool glu, const uint16_t *dy, const uint16_t *preact, const uint16_t *x,
+                               const uint16_t *w, const uint16_t *dz, const uint16_t *dx,
+                               const uint16_t *dw, const float *dbias, const void *workspace) {
+  const int rc = check_expert_op(p, op);
+  if (rc != MOE_OK) return rc;
+  if (op->fmt != MOE_FMT_BF16) return MOE_EINVAL;
+  if (!plan || !plan->expert_counts || !plan->expert_offsets) return MOE_EINVAL;
+  const bool through_act = glu || op->act != MOE_ACT_NONE;
+  // a layer without activation has dz = dy
+  if (!through_act && (preact || dz)) return MOE_EINVAL;
+  const bool rows = expert_row_bound(*p) > 0;
+  if (rows && (!dy || (through_act && (!preact || !dz)))) return MOE_EINVAL;
+  if (rows && ((dx && !w) || (dw && !x))) return MOE_EINVAL;
+  if (dbias && !workspace) return MOE_EINVAL;
+  if (!aligned(dy, 16) || !aligned(preact, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dz, 16) ||
+      !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(workspace, 256) ||
+      !aligned(plan->expert_counts, 4) || !aligned(plan->expert_offsets, 4))
     return MOE_EALIGN;
   return MOE_OK;
 }

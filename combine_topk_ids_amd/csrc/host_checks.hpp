@@ -83,6 +83,19 @@ size_t map_workspace_bytes(const moe_problem &p);
 // ceil(cf * N * k / E) in double precision, or a negative error code
 int64_t expert_capacity(int64_t n_tokens, int32_t top_k, int32_t n_experts, double cf);
 
+// Rows of the packed buffer that can hold a token: N*k, or what the fixed
+// capacity leaves of it.
+inline int64_t expert_row_bound(const moe_problem &p) {
+  const int64_t pairs = p.n_tokens * p.top_k, rows = max_rows(p);
+  return pairs < rows ? pairs : rows;
+}
+
+// Workspace of the experts' backward passes: column sums of dz over 64-row
+// chunks of each expert (at most rows / 64 + E of them, up to 2 * out_dim
+// columns), for dbias.
+constexpr int kBiasChunkRows = 64;
+size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op);
+
 // ---- argument checks: MOE_OK or the code the entry point returns -----------
 namespace host {
 
@@ -121,6 +134,21 @@ int check_exchange_combine_args(const moe_problem *p, const moe_exchange *x, con
 int check_map_args(const moe_problem *p, const uint8_t *routing_map, const float *probs,
                    const int32_t *topk_ids, const float *topk_weights, const uint32_t *status,
                    const void *workspace);
+
+int check_combine_backward_args(const moe_problem *p, const moe_plan *plan, const uint16_t *expert_out,
+                                const float *topk_weights, const uint16_t *dout, const uint16_t *dy,
+                                const float *dweights);
+
+int check_expert_op(const moe_problem *p, const moe_expert_op *op);
+// residual: the linear layer only
+int check_expert_forward_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                              const void *x, const float *x_scales, const void *w, const float *w_scales,
+                              const float *bias, const uint16_t *residual, const uint16_t *y,
+                              const uint16_t *preact);
+int check_expert_backward_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                               bool glu, const uint16_t *dy, const uint16_t *preact, const uint16_t *x,
+                               const uint16_t *w, const uint16_t *dz, const uint16_t *dx,
+                               const uint16_t *dw, const float *dbias, const void *workspace);
 
 const char *error_text(int code);
 

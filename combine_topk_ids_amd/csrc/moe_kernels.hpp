@@ -67,4 +67,29 @@ hipError_t launch_plan_dispatch(const moe_problem &p, const int32_t *ids, const 
 hipError_t launch_combine(const moe_problem &p, const moe_plan &plan, const uint16_t *expert_out,
                           int64_t rows, const float *weights, uint16_t *out, hipStream_t stream);
 
+// dy rows and dweights (either input that no output needs may be NULL): the
+// gradients of launch_combine
+hipError_t launch_combine_backward(const moe_problem &p, const moe_plan &plan, const uint16_t *expert_out,
+                                   const float *weights, const uint16_t *dout, uint16_t *dy,
+                                   float *dweights, hipStream_t stream);
+
+// The experts' products over the packed rows (glu: the gated block).
+struct ExpertForward {
+  const void *x, *w;
+  const float *x_scales, *w_scales, *bias;
+  const uint16_t *residual;
+  uint16_t *y, *preact;
+};
+hipError_t launch_expert_forward(const moe_problem &p, const moe_plan &plan, const moe_expert_op &op,
+                                 bool glu, const ExpertForward &f, hipStream_t stream);
+
+struct ExpertBackward {
+  const uint16_t *dy, *preact, *x, *w;
+  uint16_t *dz, *dx, *dw;
+  float *dbias;
+  void *workspace;
+};
+hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, const moe_expert_op &op,
+                                  bool glu, const ExpertBackward &b, hipStream_t stream);
+
 }  // namespace moe

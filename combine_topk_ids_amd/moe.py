@@ -24,6 +24,7 @@ NOALLOC_SCRATCH_BYTES = 1 << 20  # MOE_NOALLOC_SCRATCH_BYTES
 STATUS_BAD_ID, STATUS_DUP_ID, STATUS_CAPACITY, STATUS_MAP_OVERFLOW, STATUS_DROPPED = 1, 2, 4, 8, 16
 STATUS_BAD_PLAN = 32
 FMT = {"bf16": 0, "fp8": 1, "mxfp4": 2, "nvfp4": 3}
+ACT = {"none": 0, "silu": 1, "gelu_tanh": 2, "relu": 3}
 FLAG_ZERO_TAIL = 1
 # how moe_plan_and_dispatch runs a problem (moe_plan_and_dispatch_mode)
 PD_ONE_LAUNCH, PD_TILED, PD_SEPARATE = 1, 2, 3
@@ -37,7 +38,10 @@ EXPORTS = ("moe_check_problem", "moe_max_rows", "moe_expert_capacity", "moe_payl
            "moe_check_exchange", "moe_exchange_workspace_bytes", "moe_exchange_plan",
            "moe_exchange_dispatch", "moe_exchange_dispatch_scaled", "moe_exchange_dispatch_gated",
            "moe_exchange_combine", "moe_map_workspace_bytes",
-           "moe_routing_map_to_topk", "moe_plan_and_dispatch_noalloc", "moe_strerror")
+           "moe_routing_map_to_topk", "moe_plan_and_dispatch_noalloc", "moe_combine_backward",
+           "moe_check_expert_op", "moe_expert_workspace_bytes", "moe_expert_glu",
+           "moe_expert_linear", "moe_expert_glu_backward", "moe_expert_linear_backward",
+           "moe_strerror")
 
 
 class MoeError(RuntimeError):
@@ -66,6 +70,10 @@ class Exchange(ctypes.Structure):
         "recv_slot", "recv_src", "status")]
 
 
+class ExpertOp(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in ("in_dim", "out_dim", "act", "fmt")]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -73,6 +81,7 @@ def _load() -> ctypes.CDLL:
             "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, V = ctypes.POINTER(Problem), ctypes.c_void_p
+    L, O = ctypes.POINTER(Plan), ctypes.POINTER(ExpertOp)
     sig = {
         "moe_check_problem": (ctypes.c_int, [P]),
         "moe_max_rows": (ctypes.c_int64, [P]),
@@ -100,6 +109,13 @@ def _load() -> ctypes.CDLL:
         "moe_exchange_combine": (ctypes.c_int, [P, ctypes.POINTER(Exchange), V, V, V, V]),
         "moe_map_workspace_bytes": (ctypes.c_size_t, [P]),
         "moe_routing_map_to_topk": (ctypes.c_int, [P, V, V, V, V, V, V, V]),
+        "moe_combine_backward": (ctypes.c_int, [P, L] + [V] * 6),
+        "moe_check_expert_op": (ctypes.c_int, [P, O]),
+        "moe_expert_workspace_bytes": (ctypes.c_size_t, [P, O]),
+        "moe_expert_glu": (ctypes.c_int, [P, L, O] + [V] * 8),
+        "moe_expert_linear": (ctypes.c_int, [P, L, O] + [V] * 9),
+        "moe_expert_glu_backward": (ctypes.c_int, [P, L, O] + [V] * 10),
+        "moe_expert_linear_backward": (ctypes.c_int, [P, L, O] + [V] * 10),
         "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():
@@ -414,6 +430,124 @@ def moe_combine(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor,
     rc = lib.moe_combine(ctypes.byref(p), ctypes.byref(plan.as_struct()), y, w, o,
                          _stream(stream))
     _checked(rc, "moe_combine")
+
+
+def moe_combine_backward(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor | None,
+                         topk_weights: torch.Tensor | None, dout: torch.Tensor, dy: torch.Tensor,
+                         dweights: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of moe_combine: dy rows (rows that no slot names are left as
+    they were) and, unless None, dweights."""
+    r_max = _sizes(p)[0]
+    npairs = p.n_tokens * p.top_k
+    y = _dev(expert_out, "expert_out", _BF16, r_max * p.hidden) or None
+    w = _dev(topk_weights, "topk_weights", (torch.float32,), npairs) or None
+    d = _dev(dout, "dout", _BF16, p.n_tokens * p.hidden)
+    o = _dev(dy, "dy", _BF16, r_max * p.hidden)
+    dw = _dev(dweights, "dweights", (torch.float32,), npairs) or None
+    rc = lib.moe_combine_backward(ctypes.byref(p), ctypes.byref(plan.as_struct()), y, w, d, o, dw,
+                                  _stream(stream))
+    _checked(rc, "moe_combine_backward")
+
+
+# ---- the experts' products over the packed rows ---------------------------------
+
+def expert_op(in_dim: int, out_dim: int, act: str = "none", fmt: str = "bf16") -> ExpertOp:
+    """Build a moe_expert_op: in_dim columns of x and w, out_dim columns of the
+    result (the gated block's weights have 2 * out_dim rows)."""
+    return ExpertOp(in_dim, out_dim, ACT[act], FMT[fmt])
+
+
+def moe_check_expert_op(p: Problem, op: ExpertOp) -> int:
+    return int(lib.moe_check_expert_op(ctypes.byref(p), ctypes.byref(op)))
+
+
+def moe_expert_workspace_bytes(p: Problem, op: ExpertOp) -> int:
+    return int(lib.moe_expert_workspace_bytes(ctypes.byref(p), ctypes.byref(op)))
+
+
+def alloc_expert_workspace(p: Problem, op: ExpertOp, device="cuda") -> torch.Tensor:
+    """Scratch of the backward calls with a dbias."""
+    nbytes = moe_expert_workspace_bytes(p, op)
+    if nbytes == 0:
+        raise MoeError(moe_check_expert_op(p, op), "alloc_expert_workspace")
+    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _expert_forward(name, fn, wide, p, plan, op, x, w, y, x_scales, w_scales, bias, preact,
+                    residual=()):
+    rows, e, k, n = _sizes(p)[0], p.n_experts, op.in_dim, op.out_dim
+    fp8 = op.fmt == FMT["fp8"]
+    codes = (torch.uint8, torch.float8_e4m3fn) if fp8 else _BF16
+    args = [_dev(x, "x", codes, rows * k),
+            _dev(x_scales, "x_scales", (torch.float32,), rows * (k // 128)) or None,
+            _dev(w, "w", codes, e * wide * n * k),
+            _dev(w_scales, "w_scales", (torch.float32,), e * (wide * n // 128) * (k // 128)) or None,
+            _dev(bias, "bias", (torch.float32,), e * wide * n) or None]
+    args += [_dev(r, "residual", _BF16, rows * n) or None for r in residual]
+    args += [_dev(y, "y", _BF16, rows * n), _dev(preact, "preact", _BF16, rows * wide * n) or None]
+    return fn, name, (ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args)
+
+
+def moe_expert_glu(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor, w: torch.Tensor,
+                   h: torch.Tensor, x_scales: torch.Tensor | None = None,
+                   w_scales: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                   preact: torch.Tensor | None = None, stream=None) -> None:
+    """Gated block over the packed rows: h = act(z[:, :F]) * z[:, F:] with
+    z = x w_e^T + bias_e; w [E, 2F, K], gate rows first."""
+    fn, name, args = _expert_forward("moe_expert_glu", lib.moe_expert_glu, 2, p, plan, op, x, w, h,
+                                     x_scales, w_scales, bias, preact)
+    _checked(fn(*args, _stream(stream)), name)
+
+
+def moe_expert_linear(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor, w: torch.Tensor,
+                      y: torch.Tensor, x_scales: torch.Tensor | None = None,
+                      w_scales: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                      residual: torch.Tensor | None = None, preact: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """Linear layer over the packed rows: y = act(x w_e^T + bias_e) + residual;
+    w [E, F, K]."""
+    fn, name, args = _expert_forward("moe_expert_linear", lib.moe_expert_linear, 1, p, plan, op, x, w,
+                                     y, x_scales, w_scales, bias, preact, (residual,))
+    _checked(fn(*args, _stream(stream)), name)
+
+
+def _expert_backward(name, fn, wide, p, plan, op, dy, preact, x, w, dz, dx, dw, dbias, workspace,
+                     stream):
+    rows, e, k, n = _sizes(p)[0], p.n_experts, op.in_dim, op.out_dim
+    ws = moe_expert_workspace_bytes(p, op) if dbias is not None else None
+    args = (_dev(dy, "dy", _BF16, rows * n),
+            _dev(preact, "preact", _BF16, rows * wide * n) or None,
+            _dev(x, "x", _BF16, rows * k) or None,
+            _dev(w, "w", _BF16, e * wide * n * k) or None,
+            _dev(dz, "dz", _BF16, rows * wide * n) or None,
+            _dev(dx, "dx", _BF16, rows * k) or None,
+            _dev(dw, "dw", _BF16, e * wide * n * k) or None,
+            _dev(dbias, "dbias", (torch.float32,), e * wide * n) or None,
+            _dev(workspace, "workspace", (torch.uint8,), ws) or None)
+    rc = fn(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args, _stream(stream))
+    _checked(rc, name)
+
+
+def moe_expert_glu_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dh: torch.Tensor,
+                            preact: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None,
+                            dz: torch.Tensor, dx: torch.Tensor | None, dw: torch.Tensor | None,
+                            dbias: torch.Tensor | None = None,
+                            workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of moe_expert_glu; dx, dw and dbias may be None (not
+    computed).  dbias needs a workspace (alloc_expert_workspace)."""
+    _expert_backward("moe_expert_glu_backward", lib.moe_expert_glu_backward, 2, p, plan, op, dh,
+                     preact, x, w, dz, dx, dw, dbias, workspace, stream)
+
+
+def moe_expert_linear_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dy: torch.Tensor,
+                               x: torch.Tensor | None, w: torch.Tensor | None,
+                               dx: torch.Tensor | None, dw: torch.Tensor | None,
+                               preact: torch.Tensor | None = None, dz: torch.Tensor | None = None,
+                               dbias: torch.Tensor | None = None,
+                               workspace: torch.Tensor | None = None, stream=None) -> None:
+    """Gradients of moe_expert_linear; preact and dz with an activation only."""
+    _expert_backward("moe_expert_linear_backward", lib.moe_expert_linear_backward, 1, p, plan, op, dy,
+                     preact, x, w, dz, dx, dw, dbias, workspace, stream)
 
 
 # ---- exchange across EP simulated ranks ---------------------------------------

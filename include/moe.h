@@ -338,6 +338,120 @@ MOE_API int moe_combine(const moe_problem *p, const moe_plan *plan,
                         const uint16_t *expert_out, const float *topk_weights,
                         uint16_t *out, void *stream);
 
+/* Gradients of the combine, for a training step: from dout = d loss / d out
+ * (device bf16 bits [N][H]),
+ *   dy[slot[t][j]][c] = bf16_rne(fl32(topk_weights[t][j] * dout[t][c])),
+ *   dweights[t][j]    = sum over c of expert_out[slot[t][j]][c] * dout[t][c]
+ *                       (fp32, in a fixed order; 0 for a masked pair).
+ * Rows of dy that no slot names are left as they were, and rows of expert_out
+ * that no slot names are not read.  topk_weights NULL: the unweighted combine
+ * (dy rows are copies of dout); dweights must then be NULL.  dweights NULL: it
+ * is not computed and expert_out is not read (it may be NULL).  expert_out, dy:
+ * device bf16 bits [R_max][H]; dweights: device float [N][k].
+ * The gradient of a dispatch is a combine: with NULL weights for moe_dispatch,
+ * with the gates for moe_dispatch_gated, whose gates' gradient is this call's
+ * dweights with the dispatch's hidden rows for dout and the packed rows'
+ * gradient for expert_out. */
+MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
+                                 const uint16_t *expert_out, const float *topk_weights,
+                                 const uint16_t *dout, uint16_t *dy, float *dweights,
+                                 void *stream);
+
+/* ---- the experts' products over the packed rows ------------------------------
+ *
+ * Between dispatch and combine: every expert's matrix product over its rows of
+ * the packed buffer, with the row ranges read from the plan on the device
+ * (expert_offsets, expert_counts; no host wait).  Rows that hold no token --
+ * pad rows, rows past R_used, unused rows of a fixed capacity -- are neither
+ * read nor written, and an expert without rows costs nothing.  Whatever the plan
+ * arrays hold, no access leaves [0, R_max).
+ *
+ * Sums are fp32 (MFMA accumulators); results are rounded to bf16 once, when they
+ * are stored.  Each result depends on its own row, weights and bias alone, and
+ * runs repeat bit for bit.  An infinity or NaN in a row or in an expert's weights
+ * reaches the results of that row or expert only.
+ *
+ * p names the packed buffer (R_max rows, E experts); its hidden and fmt are not
+ * used here.  Needs in_dim, out_dim <= 2^20, in_dim * out_dim < 2^29 and
+ * (rows / 64 + E) * max(in_dim, 2 * out_dim) / 64 < 2^22 (MOE_EOVERFLOW). */
+typedef enum moe_act {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_SILU = 1,      /* z * sigmoid(z)                                    */
+  MOE_ACT_GELU_TANH = 2, /* z/2 * (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   */
+  MOE_ACT_RELU = 3       /* max(z, 0); its slope at 0 is 0                    */
+} moe_act;
+
+typedef struct moe_expert_op { /* host memory */
+  int32_t in_dim;  /* K > 0: columns of a row of x and of the weights        */
+  int32_t out_dim; /* F > 0: columns of a row of h or y                      */
+  int32_t act;     /* a moe_act value                                        */
+  int32_t fmt;     /* of x and w (results are bf16):
+                      MOE_FMT_BF16: K, F multiples of 8;
+                      MOE_FMT_FP8_E4M3_B128 (K, F multiples of 128): x as
+                      moe_dispatch writes it (codes [R_max][K], scales float
+                      [R_max][K/128]); w E4M3 codes with one fp32 scale per
+                      128x128 block, w_scales float [E][rows/128][K/128]; a
+                      value is code * scale.  Forward passes only.           */
+} moe_expert_op;
+
+/* MOE_OK if op is well formed for p, else the code the calls below return. */
+MOE_API int moe_check_expert_op(const moe_problem *p, const moe_expert_op *op);
+
+/* Device scratch bytes of the backward calls with a dbias (0 for an invalid
+ * op).  256-byte aligned, caller-owned, needs no initialisation; two calls
+ * that may overlap (two streams, two captured graphs) need one each. */
+MOE_API size_t moe_expert_workspace_bytes(const moe_problem *p, const moe_expert_op *op);
+
+/* Gated feed-forward block, both projections in one pass over x: for a row of
+ * expert e
+ *   z = x w_e^T + bias_e (2F values),  h = act(z[0..F)) * z[F..2F).
+ * x: rows [R_max][K] (p->fmt's bf16 or FP8 payload, see moe_expert_op); w:
+ * device [E][2F][K], the gate's F rows first, then the up projection's; bias:
+ * device float [E][2F] or NULL; h: device bf16 bits [R_max][F]; preact: device
+ * bf16 bits [R_max][2F] for z, which the backward pass reads, or NULL.  (h is
+ * computed from the unrounded z.) */
+MOE_API int moe_expert_glu(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                           const void *x, const float *x_scales, const void *w,
+                           const float *w_scales, const float *bias, uint16_t *h,
+                           uint16_t *preact, void *stream);
+
+/* Linear layer with its epilogue: y = act(x w_e^T + bias_e) + residual.  w:
+ * device [E][F][K]; bias: device float [E][F] or NULL; residual: device bf16
+ * bits [R_max][F] or NULL (it may be y itself); y: [R_max][F]; preact: device
+ * bf16 bits [R_max][F] for z = x w_e^T + bias_e, or NULL. */
+MOE_API int moe_expert_linear(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                              const void *x, const float *x_scales, const void *w,
+                              const float *w_scales, const float *bias,
+                              const uint16_t *residual, uint16_t *y, uint16_t *preact,
+                              void *stream);
+
+/* Gradients of moe_expert_glu from dh (bf16 [R_max][F]), the preact that it
+ * kept, x and w (bf16):
+ *   dz = (dh * up * act'(gate), dh * act(gate))   bf16 [R_max][2F]
+ *   dx = dz w_e                                    bf16 [R_max][K]
+ *   dw_e = dz^T x over the expert's rows           bf16 [E][2F][K]
+ *   dbias_e = sum of dz over the expert's rows     float [E][2F]
+ * dz is an output and required: it is rounded to bf16 there, and dx and dw are
+ * products of the rounded values; dbias sums the unrounded ones.  dx, dw and
+ * dbias may each be NULL (not computed).  dw and dbias are written whole, zeros
+ * for experts without rows.  workspace: moe_expert_workspace_bytes, needed
+ * with dbias only. */
+MOE_API int moe_expert_glu_backward(const moe_problem *p, const moe_plan *plan,
+                                    const moe_expert_op *op, const uint16_t *dh,
+                                    const uint16_t *preact, const uint16_t *x,
+                                    const uint16_t *w, uint16_t *dz, uint16_t *dx, uint16_t *dw,
+                                    float *dbias, void *workspace, void *stream);
+
+/* Gradients of moe_expert_linear: as above with dz = dy * act'(preact), bf16
+ * [R_max][F].  Without activation dz is dy itself, and preact and dz must be
+ * NULL.  The residual's gradient is dy. */
+MOE_API int moe_expert_linear_backward(const moe_problem *p, const moe_plan *plan,
+                                       const moe_expert_op *op, const uint16_t *dy,
+                                       const uint16_t *preact, const uint16_t *x,
+                                       const uint16_t *w, uint16_t *dz, uint16_t *dx,
+                                       uint16_t *dw, float *dbias, void *workspace,
+                                       void *stream);
+
 /* ---- exchange across EP simulated ranks ----------------------------------
  *
  * One GPU holds the shares of all EP ranks of an expert-parallel group: rank
