@@ -28,23 +28,14 @@ struct GradArgs {
   int n_experts, rows, n, width, col_tiles;
 };
 
-__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8]) {
-  unpack8(*reinterpret_cast<const uint4 *>(p), v);
-}
-__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
-  typedef __bf16 bf16x8s __attribute__((ext_vector_type(8)));
-  bf16x8s r;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) r[c] = static_cast<__bf16>(v[c]);
-  *reinterpret_cast<bf16x8s *>(p) = r;
-}
-
 // One workgroup: up to 64 rows of one expert x 512 columns; a wave walks every
 // fourth row.  Memory bound: each input is read and each output written once.
 template <bool GLU, int ACT>
 __global__ __launch_bounds__(kWaves *kWave) void grad_kernel(GradArgs g) {
   __shared__ float sums[kWaves][2][kSlabCols];
-  const RowTile t = find_row_tile<kChunkRows>(g.offsets, g.counts, g.n_experts, g.rows, g.col_tiles);
+  RowTiles<kChunkRows> order;
+  order.init(g.offsets, g.counts, g.n_experts, g.rows, g.col_tiles);
+  const RowTile t = order.find(0);
   if (t.e < 0) return;
   const int wave = wave_id(), col = t.j * kSlabCols + lane_id() * 8;
   const bool live = col < g.n;
@@ -131,78 +122,122 @@ struct ProductArgs {
   int col_tiles;
 };
 
-__device__ __forceinline__ bf16x4 to_bf16(const f32x4 v) {
-  bf16x4 r;
+// Results of a wave, to a tile of rows x cols of `out`, whose rows have `ld`
+// columns.  Returns the wave's stores.
+template <class S, int FI>
+__device__ __forceinline__ int store_tile(lds_ptr lds, const f32x4 (&acc)[FI][S::FJ], uint16_t *out, int ld,
+                                          int rows, int cols) {
+  constexpr int kCols = S::BJ / S::WJ;
+  static_assert(S::WI * S::WJ * Transpose<kCols>::kBytes <= S::kStage, "a region for each wave");
+  const Wave<S> w = this_wave<S>();
+  const Transpose<kCols> turn{lds + (S::NST - 1) * S::kStage + wave_id() * Transpose<kCols>::kBytes,
+                              late_lane_id()};
+  const int col = w.wj * kCols + turn.col();
+  const auto r = buffer_rsrc(out, kRecords);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) r[i] = static_cast<__bf16>(v[i]);
-  return r;
+  for (int a = 0; a < FI; ++a) {
+#pragma unroll
+    for (int b = 0; b < S::FJ; ++b) turn.put(b, acc[a][b]);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < turn.kPasses; ++p) {
+      const int i = (w.wi + a * S::WI) * 16 + turn.row(p);
+      float v[8];
+      turn.get(p, v);
+      store8(r, i < rows && col < cols ? static_cast<uint32_t>(i * ld + col) * 2 : kNowhere, v);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  return FI * Transpose<kCols>::kPasses;
 }
 
 template <class S>
 __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dx_kernel(ProductArgs g) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
-  const RowTile t = find_row_tile<S::BI>(g.offsets, g.counts, g.n_experts, g.rows, g.col_tiles);
-  if (t.e < 0) return;
-  const int row_bytes = g.n * 2, j0 = t.j * S::BJ;
-  const int wave = wave_id(), wi = wave / S::WJ, wj = wave % S::WJ, lane = lane_id();
+  lds_ptr lds = (lds_ptr)smem;
+  const int row_bytes = g.n * 2, steps = (g.n + S::kStepRows - 1) / S::kStepRows;
+  RowTiles<S::BI> order;
+  order.init(g.offsets, g.counts, g.n_experts, g.rows, g.col_tiles);
   AlongLoader<S, S::LI> li;
-  li.init(g.dz + (static_cast<int64_t>(t.start) + t.i0) * g.n, row_bytes, [&](int r) {
-    return r < S::BI && t.i0 + r < t.count ? static_cast<uint32_t>(r * row_bytes) : kNowhere;
-  });
   AcrossLoader<S, S::BJ, S::LJ> lj;
-  lj.init(g.w + static_cast<int64_t>(t.e) * g.n * g.k + j0, static_cast<int64_t>(g.k) * 2, g.n, g.k - j0);
-  f32x4 acc[S::FI][S::FJ];
-  multiply<S>((lds_ptr)smem, (g.n + kStepRows - 1) / kStepRows, li, lj, NoScales(), [](int) { return 0; },
-              wi, wj, acc);
-#pragma unroll
-  for (int b = 0; b < S::FJ; ++b) {
-    const int col = j0 + (wj * S::FJ + b) * 16 + (lane >> 4) * 4;
-    if (col >= g.k) continue;
-#pragma unroll
-    for (int a = 0; a < S::FI; ++a) {
-      const int i = t.i0 + (wi * S::FI + a) * 16 + (lane & 15);
-      if (i < t.count)
-        *reinterpret_cast<bf16x4 *>(g.out + (static_cast<int64_t>(t.start) + i) * g.k + col) =
-            to_bf16(acc[a][b]);
-    }
+  auto begin = [&](const RowTile &t) {
+    const int j0 = t.j * S::BJ;
+    li.init(g.dz + (static_cast<int64_t>(t.start) + t.i0) * g.n, row_bytes, [&](int r) {
+      return r < S::BI && t.i0 + r < t.count ? static_cast<uint32_t>(r * row_bytes) : kNowhere;
+    });
+    lj.init(g.w + static_cast<int64_t>(t.e) * g.n * g.k + j0, static_cast<int64_t>(g.k) * 2, g.n, g.k - j0);
+    start<S>(lds, steps, li, lj, NoScales());
+  };
+  RowTile t = order.find(0);
+  if (t.e < 0) return;
+  begin(t);
+  RowTile next;
+  int younger = 0;  // stores after the tile's first loads
+  auto one_tile = [&](auto blocks) {
+    constexpr int FI = decltype(blocks)::value;
+    f32x4 acc[FI][S::FJ];
+    multiply<S, FI>(lds, steps, li, lj, NoScales(), [](int) { return 0; }, younger, acc);
+    if (next.e >= 0) begin(next);
+    younger = store_tile<S, FI>(lds, acc, g.out + (static_cast<int64_t>(t.start) + t.i0) * g.k + t.j * S::BJ, g.k,
+                      t.count - t.i0, g.k - t.j * S::BJ);
+  };
+  for (int n = 1; t.e >= 0; ++n) {
+    next = order.find(n);
+    with_blocks<S>(t.count - t.i0, one_tile);
+    t = next;
   }
 }
 
 // ---- dw = dz^T x -----------------------------------------------------------------
 
-// One workgroup a BI x BJ tile of one expert's dw: the contraction runs over
-// the expert's rows, none of them for an expert without rows (its dw is zeros).
+// BI x BJ tiles of the experts' dw: the contraction runs over the expert's rows,
+// none of them for an expert without rows (its dw is zeros).  An XCD takes one
+// run of tiles, expert by expert: the expert's rows stay in its L2.
 template <class S>
-__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(ProductArgs g, int row_tiles, int total) {
+__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(ProductArgs g, int row_tiles,
+                                                                           int total) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
-  // an XCD takes one run of tiles, expert by expert: its rows stay in that L2
-  const int chunk = (total + 7) / 8, pos = blockIdx.x / 8;
-  const int64_t id = static_cast<int64_t>(blockIdx.x % 8) * chunk + pos;
-  if (pos >= chunk || id >= total) return;
-  const int per = row_tiles * g.col_tiles;
-  const int e = static_cast<int>(id / per), q = static_cast<int>(id - static_cast<int64_t>(e) * per);
-  const int group = q / (8 * g.col_tiles), rest = q - group * 8 * g.col_tiles;
-  const int size = min(8, row_tiles - group * 8);
-  const int j0 = rest / size * S::BJ, i0 = (group * 8 + rest % size) * S::BI;
-  const ExpertRows r = expert_rows(g.offsets, g.counts, e, g.rows);
-  const int wave = wave_id(), wi = wave / S::WJ, wj = wave % S::WJ, lane = lane_id();
+  lds_ptr lds = (lds_ptr)smem;
+  const int chunk = (total + 7) / 8, per = row_tiles * g.col_tiles;
   AcrossLoader<S, S::BI, S::LI> li;
-  li.init(g.dz + static_cast<int64_t>(r.start) * g.n + i0, static_cast<int64_t>(g.n) * 2, r.count, g.n - i0);
   AcrossLoader<S, S::BJ, S::LJ> lj;
-  lj.init(g.x + static_cast<int64_t>(r.start) * g.k + j0, static_cast<int64_t>(g.k) * 2, r.count, g.k - j0);
-  f32x4 acc[S::FI][S::FJ];
-  multiply<S>((lds_ptr)smem, (r.count + kStepRows - 1) / kStepRows, li, lj, NoScales(),
-              [](int) { return 0; }, wi, wj, acc);
-  uint16_t *out = g.out + static_cast<int64_t>(e) * g.n * g.k;
-#pragma unroll
-  for (int b = 0; b < S::FJ; ++b) {
-    const int col = j0 + (wj * S::FJ + b) * 16 + (lane >> 4) * 4;
-    if (col >= g.k) continue;
-#pragma unroll
-    for (int a = 0; a < S::FI; ++a) {
-      const int i = i0 + (wi * S::FI + a) * 16 + (lane & 15);
-      if (i < g.n) *reinterpret_cast<bf16x4 *>(out + static_cast<int64_t>(i) * g.k + col) = to_bf16(acc[a][b]);
-    }
+  struct Tile {
+    int e, i0, j0, steps;
+  };
+  auto find = [&](int n) {
+    Tile t{-1, 0, 0, 0};
+    const int64_t pos = blockIdx.x / 8 + static_cast<int64_t>(n) * (gridDim.x / 8);
+    const int64_t id = (blockIdx.x % 8) * static_cast<int64_t>(chunk) + pos;
+    if (pos >= chunk || id >= total) return t;
+    t.e = static_cast<int>(id / per);
+    const int q = static_cast<int>(id - static_cast<int64_t>(t.e) * per);
+    const int group = q / (8 * g.col_tiles), rest = q - group * 8 * g.col_tiles;
+    const int size = min(8, row_tiles - group * 8);
+    t.j0 = rest / size * S::BJ;
+    t.i0 = (group * 8 + rest % size) * S::BI;
+    return t;
+  };
+  auto begin = [&](Tile &t) {
+    const ExpertRows r = expert_rows(g.offsets, g.counts, t.e, g.rows);
+    t.steps = (r.count + S::kStepRows - 1) / S::kStepRows;
+    li.init(g.dz + static_cast<int64_t>(r.start) * g.n + t.i0, static_cast<int64_t>(g.n) * 2, r.count,
+            g.n - t.i0);
+    lj.init(g.x + static_cast<int64_t>(r.start) * g.k + t.j0, static_cast<int64_t>(g.k) * 2, r.count,
+            g.k - t.j0);
+    start<S>(lds, t.steps, li, lj, NoScales());
+  };
+  Tile t = find(0);
+  if (t.e < 0) return;
+  begin(t);
+  int younger = 0;  // stores after the tile's first loads
+  for (int n = 1; t.e >= 0; ++n) {
+    f32x4 acc[S::FI][S::FJ];
+    multiply<S, S::FI>(lds, t.steps, li, lj, NoScales(), [](int) { return 0; }, younger, acc);
+    Tile next = find(n);
+    if (next.e >= 0) begin(next);
+    younger = store_tile<S, S::FI>(lds, acc, g.out + (static_cast<int64_t>(t.e) * g.n + t.i0) * g.k + t.j0, g.k, g.n - t.i0,
+                  g.k - t.j0);
+    t = next;
   }
 }
 
@@ -211,7 +246,7 @@ hipError_t launch_dx(ProductArgs g, int64_t pairs, hipStream_t stream) {
   g.col_tiles = (g.k + S::BJ - 1) / S::BJ;
   const int64_t tiles = row_tile_bound<S::BI>(pairs, g.n_experts) * g.col_tiles;
   if (tiles == 0) return hipSuccess;
-  dx_kernel<S><<<static_cast<uint32_t>((tiles + 7) / 8 * 8), S::kThreads, 0, stream>>>(g);
+  dx_kernel<S><<<tile_grid(tiles, S::kResident), S::kThreads, 0, stream>>>(g);
   return hipGetLastError();
 }
 
@@ -220,8 +255,8 @@ hipError_t launch_dw(ProductArgs g, hipStream_t stream) {
   g.col_tiles = (g.k + S::BJ - 1) / S::BJ;
   const int row_tiles = (g.n + S::BI - 1) / S::BI;
   const int64_t total = static_cast<int64_t>(g.n_experts) * row_tiles * g.col_tiles;
-  dw_kernel<S><<<static_cast<uint32_t>((total + 7) / 8 * 8), S::kThreads, 0, stream>>>(
-      g, row_tiles, static_cast<int>(total));
+  dw_kernel<S><<<tile_grid(total, S::kResident), S::kThreads, 0, stream>>>(g, row_tiles,
+                                                                          static_cast<int>(total));
   return hipGetLastError();
 }
 
@@ -265,12 +300,12 @@ hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, co
   a.n = width;
   if (b.dx) {
     a.out = b.dx;
-    err = launch_dx<Shape<128, 128, 2, 2, 2, false, true>>(a, pairs, stream);
+    err = launch_dx<Shape<256, 256, 2, 4, 128, 2, false, true>>(a, pairs, stream);
     if (err != hipSuccess) return err;
   }
   if (b.dw) {
     a.out = b.dw;
-    err = launch_dw<Shape<128, 128, 2, 2, 2, true, true>>(a, stream);
+    err = launch_dw<Shape<256, 256, 2, 4, 128, 2, true, true>>(a, stream);
   }
   return err;
 }

@@ -11,16 +11,16 @@
 // J is the MFMA's A operand and I its B operand, so that a lane ends with four
 // neighbouring j of one i: 8-byte stores of bf16, and one row scale per lane.
 //
-// Memory path.  A step covers 128 bytes of the contraction (64 bf16 or 128
-// E4M3 values).  Tiles go from global memory straight into LDS (16 bytes a
+// Memory path.  A step covers SB = 64 or 128 bytes of the contraction (32 or 64
+// bf16, 128 E4M3 values).  Tiles go from global memory straight into LDS (16 bytes a
 // lane, no registers), NST stages deep: the loads of step t + NST - 1 are
 // issued before the products of step t, and one barrier a step both publishes
 // a stage and frees the one before it.  Such a load writes 64 consecutive 16-byte chunks of
 // LDS, so there is no padding against bank conflicts; instead a lane picks which
 // chunk of its row it fetches:
-//   along c:  rows of 8 chunks, chunk c of row r at position c ^ (r & 7); the
-//             16-byte operand reads of 8 consecutive lanes (8 rows, one chunk
-//             index) then touch 8 different positions;
+//   along c:  rows of SB / 16 chunks, chunk c of row r at along_chunk(r, c):
+//             the 16-byte operand reads of 8 consecutive lanes (8 rows, one
+//             chunk index) then touch 8 different 16-byte bank groups;
 //   across c: rows of 16-column groups (32 bytes), group g of row r at
 //             g ^ f(r), f taking r's bits 0, 1, 3, 4: the 16 rows that one
 //             transposing read visits for one group then lie in different banks.
@@ -46,33 +46,38 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef MOE_LDS char *lds_ptr;
 
-constexpr int kStepBytes = 128;  // contraction bytes of one step
-constexpr int kStepRows = 64;    // contraction rows of one step, stored across c
 // An offset past every buffer resource used here (their size is 2^31 - 1).
 constexpr uint32_t kNowhere = 0x80000000u;
 constexpr uint32_t kRecords = 0x7FFFFFFFu;
 
 // WI x WJ waves; each owns FI x FJ blocks of 16 x 16.  XI/XJ: the operand is
 // stored across c.  FP8: E4M3 codes (along c only) with block scales.
-template <int BI_, int BJ_, int WI_, int WJ_, int NST_, bool XI_ = false, bool XJ_ = false,
+template <int BI_, int BJ_, int WI_, int WJ_, int SB_, int NST_, bool XI_ = false, bool XJ_ = false,
           bool FP8_ = false>
 struct Shape {
   static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_;
+  static constexpr int SB = SB_;          // contraction bytes of one step
+  static constexpr int kStepRows = SB / 2;  // contraction rows of one step, stored across c
+  static constexpr int kChunks = SB / 16;   // 16-byte chunks of a step's row
+  
   static constexpr bool XI = XI_, XJ = XJ_, FP8 = FP8_;
   static constexpr int kThreads = WI * WJ * kWave;
   // at least two waves a SIMD: that also keeps the accumulators in the 256
   // registers that both operands and results of an MFMA can name (with more, the
   // compiler moves them to and from the accumulation registers in the loop)
-  static constexpr int kWavesPerSimd = 2;
+  static constexpr int kWavesPerSimd = BI * BJ / (WI * WJ) > 128 * 64 ? 1 : 2;
   static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
   // 16-byte loads a thread makes for an operand in a step; a tile smaller than one load
   // of every thread still gets a whole one (its spare rows are zeros)
-  static constexpr int loads(int b) { return (b * 8 + kThreads - 1) / kThreads; }
+  static constexpr int loads(int b) { return (b * kChunks + kThreads - 1) / kThreads; }
   static constexpr int LI = loads(BI), LJ = loads(BJ);
   static constexpr int kBytesI = LI * kThreads * 16, kBytesJ = LJ * kThreads * 16;
   static constexpr int kBytesScale = FP8 ? kThreads * 4 : 0;  // of each operand
   static constexpr int kStage = kBytesI + kBytesJ + 2 * kBytesScale;
   static constexpr int kLdsBytes = NST * kStage;
+  // workgroups that a compute unit holds: LDS, and two waves a SIMD
+  static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 4 * kWavesPerSimd / (WI * WJ);
+  static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
   static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // in flight per stage and wave
   static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
   static_assert(kLoads * (NST - 2) < 64, "the wait counter holds 63 loads");
@@ -89,6 +94,12 @@ __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, lds_ptr to,
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, static_cast<int>(off), 0, 0, 0);
 }
 
+// Position of chunk c of row r in an operand stored along c (and back).
+template <int SB>
+__device__ __forceinline__ int along_chunk(int r, int c) {
+  return SB == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+}
+
 // Rows stored along c.  row_offset(r): byte offset from `base` of tile row r,
 // or kNowhere; row_bytes: bytes of a whole row (a multiple of 16).
 template <class S, int L>
@@ -103,15 +114,15 @@ struct AlongLoader {
     base = static_cast<const char *>(b);
     row_bytes = bytes;
     const int tid = threadIdx.x;
-    chunk = ((tid & 7) ^ ((tid >> 3) & 7)) * 16;
+    chunk = along_chunk<S::SB>(tid / S::kChunks, tid % S::kChunks) * 16;
 #pragma unroll
     for (int u = 0; u < L; ++u) {
-      const uint32_t o = row_offset((u * S::kThreads + tid) >> 3);
+      const uint32_t o = row_offset((u * S::kThreads + tid) / S::kChunks);
       off[u] = o == kNowhere ? kNowhere : o + chunk;
     }
   }
   __device__ __forceinline__ void issue(lds_ptr to, int step) const {
-    const int at = step * kStepBytes;
+    const int at = step * S::SB;
     const auto r = buffer_rsrc(base + at, kRecords);
     const bool ok = at + chunk < row_bytes;
     const int wave = wave_id();
@@ -133,7 +144,7 @@ template <class S, int B, int L>
 struct AcrossLoader {
   static constexpr int kChunks = B / 8;                 // 16-byte chunks of a tile row
   static constexpr int kRowStep = S::kThreads / kChunks;  // rows between a thread's loads
-  static_assert(kStepRows * kChunks % S::kThreads == 0, "whole loads");
+  static_assert(S::kStepRows * kChunks % S::kThreads == 0, "whole loads");
   const char *base;
   int64_t ld;
   int rows;
@@ -152,8 +163,8 @@ struct AcrossLoader {
     }
   }
   __device__ __forceinline__ void issue(lds_ptr to, int step) const {
-    const auto r = buffer_rsrc(base + step * kStepRows * ld, kRecords);
-    const int left = rows - step * kStepRows - static_cast<int>(threadIdx.x) / kChunks;
+    const auto r = buffer_rsrc(base + step * S::kStepRows * ld, kRecords);
+    const int left = rows - step * S::kStepRows - static_cast<int>(threadIdx.x) / kChunks;
     const int wave = wave_id();
 #pragma unroll
     for (int u = 0; u < L; ++u)
@@ -182,31 +193,32 @@ struct NoScales {};
 
 // ------------------------------------------------------------- operands ---
 
-// Where a lane finds its part of an operand's 16-row blocks in a stage.
-template <int F, int B, bool X>
+// Where a lane finds its part of its wave's 16-row blocks in a stage: block b of
+// the wave is block first + b * STRIDE of the tile.
+template <int F, int B, int SB, int STRIDE, bool X>
 struct Fragments;
 
-template <int F, int B>
-struct Fragments<F, B, false> {
+template <int F, int B, int SB, int STRIDE>
+struct Fragments<F, B, SB, STRIDE, false> {
   int at[2];  // contraction halves of the step
   __device__ __forceinline__ void init(int first_block) {
     const int l = lane_id();
-    at[0] = first_block * 16 * kStepBytes + (l & 15) * kStepBytes + (((l >> 4) ^ (l & 7)) * 16);
+    at[0] = first_block * 16 * SB + (l & 15) * SB + along_chunk<SB>(l & 15, l >> 4) * 16;
     at[1] = at[0] ^ 64;
   }
   __device__ __forceinline__ i32x4 read(lds_ptr t, int b, int half) const {
-    return *(MOE_LDS const i32x4 *)(t + at[half] + b * 16 * kStepBytes);
+    return *(MOE_LDS const i32x4 *)(t + at[half] + b * STRIDE * 16 * SB);
   }
 };
 
-template <int F, int B>
-struct Fragments<F, B, true> {
+template <int F, int B, int SB, int STRIDE>
+struct Fragments<F, B, SB, STRIDE, true> {
   int at[F];
   __device__ __forceinline__ void init(int first_block) {
     const int l = lane_id(), q = l >> 4, r = q * 8 + ((l >> 2) & 3);
 #pragma unroll
     for (int b = 0; b < F; ++b)
-      at[b] = r * B * 2 + ((first_block + b) ^ group_mix<B / 16>(r)) * 32 + (l & 3) * 8;
+      at[b] = r * B * 2 + ((first_block + b * STRIDE) ^ group_mix<B / 16>(r)) * 32 + (l & 3) * 8;
   }
   // two transposing reads: contraction rows 8q .. 8q+3 and 8q+4 .. 8q+7 of the half
   __device__ __forceinline__ i32x4 read(lds_ptr t, int b, int half) const {
@@ -228,49 +240,101 @@ __device__ __forceinline__ void wait_and_meet() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-// acc[fi][fj] += the products of `steps` steps.  scale_j(fj): index of the
-// weights' scale of block fj in the stage's scale row (FP8 only).
-template <class S, class LoadI, class LoadJ, class Scales, class ScaleJ>
-__device__ __forceinline__ void multiply(lds_ptr lds, int steps, const LoadI &li, const LoadJ &lj,
-                                         const Scales &sc, ScaleJ scale_j, int wi, int wj,
-                                         f32x4 (&acc)[S::FI][S::FJ]) {
-  Fragments<S::FI, S::BI, S::XI> fi;
-  Fragments<S::FJ, S::BJ, S::XJ> fj;
-  fi.init(wi * S::FI);
-  fj.init(wj * S::FJ);
+// Order of half a step: an operand read, then some of its products, and so
+// on.  Left alone, the compiler sinks each read to just before its use, to save
+// registers, and waits for it there.
+template <int READS, int PRODUCTS>
+__device__ __forceinline__ void interleave() {
+  constexpr int kEach = PRODUCTS / READS > 0 ? PRODUCTS / READS : 1;
 #pragma unroll
-  for (int a = 0; a < S::FI; ++a)
+  for (int i = 0; i < READS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);      // LDS read
+    __builtin_amdgcn_sched_group_barrier(0x008, kEach, 0);  // MFMA
+  }
+  __builtin_amdgcn_sched_group_barrier(0x008, PRODUCTS, 0);
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+template <class S>
+struct Wave {
+  int wi, wj;  // wi owns blocks wi, wi + WI, ... of I (so that a tile with few rows leaves
+               // every wave the same share); wj a run of FJ blocks of J
+};
+template <class S>
+__device__ __forceinline__ Wave<S> this_wave() {
+  const int w = wave_id();
+  return {w / S::WJ, w % S::WJ};
+}
+
+template <class S, class LoadI, class LoadJ, class Scales>
+__device__ __forceinline__ void issue_stage(lds_ptr lds, int step, int stage, int steps, const LoadI &li,
+                                            const LoadJ &lj, const Scales &sc) {
+  lds_ptr to = lds + stage * S::kStage;
+  li.issue(to, step);
+  lj.issue(to + S::kBytesI, step);
+  if constexpr (S::FP8) sc.template issue<S>(to + S::kBytesI + S::kBytesJ, step, steps);
+}
+
+// The loads of a tile's first NST - 1 steps, into stages 0 .. NST - 2.
+template <class S, class LoadI, class LoadJ, class Scales>
+__device__ __forceinline__ void start(lds_ptr lds, int steps, const LoadI &li, const LoadJ &lj,
+                                      const Scales &sc) {
+#pragma unroll
+  for (int s = 0; s < S::NST - 1; ++s) issue_stage<S>(lds, s, s, steps, li, lj, sc);
+}
+
+// The first wait of a tile: start()'s loads are older than the `younger` stores
+// with which the wave let the last tile go, and those need not be waited for.
+// (The counter runs down in the order of issue; a smaller count waits longer.)
+template <class S>
+__device__ __forceinline__ void wait_first(int younger) {
+  constexpr int kLater = S::kLoads * (S::NST - 2);
+  if (younger >= 16)
+    wait_and_meet<kLater + 16 < 64 ? kLater + 16 : 63>();
+  else if (younger >= 8)
+    wait_and_meet<kLater + 8 < 64 ? kLater + 8 : 63>();
+  else
+    wait_and_meet<kLater>();
+}
+
+// acc[a][b] = the products of `steps` steps after start(), for the wave's first FI
+// blocks of I.  younger: see wait_first.  scale_j(b): index of the weights' scale
+// of block b in the stage's scale row (FP8 only).
+template <class S, int FI, class LoadI, class LoadJ, class Scales, class ScaleJ>
+__device__ __forceinline__ void multiply(lds_ptr lds, int steps, const LoadI &li, const LoadJ &lj,
+                                         const Scales &sc, ScaleJ scale_j, int younger,
+                                         f32x4 (&acc)[FI][S::FJ]) {
+  const Wave<S> w = this_wave<S>();
+  Fragments<FI, S::BI, S::SB, S::WI, S::XI> fi;
+  Fragments<S::FJ, S::BJ, S::SB, 1, S::XJ> fj;
+  fi.init(w.wi);
+  fj.init(w.wj * S::FJ);
+#pragma unroll
+  for (int a = 0; a < FI; ++a)
 #pragma unroll
     for (int b = 0; b < S::FJ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  auto issue = [&](int step, int stage) {
-    lds_ptr to = lds + stage * S::kStage;
-    li.issue(to, step);
-    lj.issue(to + S::kBytesI, step);
-    if constexpr (S::FP8) sc.template issue<S>(to + S::kBytesI + S::kBytesJ, step, steps);
-  };
-#pragma unroll
-  for (int s = 0; s < S::NST - 1; ++s) issue(s, s);
-  int stage = 0;
-  for (int t = 0; t < steps; ++t) {
-    wait_and_meet<S::kLoads *(S::NST - 2)>();
-    // the stage that every wave has just finished reading
-    issue(t + S::NST - 1, stage == 0 ? S::NST - 1 : stage - 1);
-    lds_ptr ti = lds + stage * S::kStage, tj = ti + S::kBytesI;
-    if constexpr (S::FP8) {
+  if constexpr (S::FP8) {
+    int stage = 0;
+    for (int t = 0; t < steps; ++t) {
+      wait_first<S>(t == 0 ? younger : 0);
+      // the stage that every wave has just finished reading
+      issue_stage<S>(lds, t + S::NST - 1, stage == 0 ? S::NST - 1 : stage - 1, steps, li, lj, sc);
+      lds_ptr ti = lds + stage * S::kStage, tj = ti + S::kBytesI;
       lds_ptr ts = tj + S::kBytesJ;
-      float si[S::FI], sj[S::FJ];
+      float si[FI], sj[S::FJ];
 #pragma unroll
-      for (int a = 0; a < S::FI; ++a)
-        si[a] = *(MOE_LDS const float *)(ts + ((wi * S::FI + a) * 16 + (lane_id() & 15)) * 4);
+      for (int a = 0; a < FI; ++a)
+        si[a] = *(MOE_LDS const float *)(ts + ((w.wi + a * S::WI) * 16 + (lane_id() & 15)) * 4);
 #pragma unroll
-      for (int b = 0; b < S::FJ; ++b) sj[b] = *(MOE_LDS const float *)(ts + S::kBytesScale + scale_j(b) * 4);
+      for (int b = 0; b < S::FJ; ++b)
+        sj[b] = *(MOE_LDS const float *)(ts + S::kBytesScale + scale_j(b) * 4);
       i32x8 vj[S::FJ];
 #pragma unroll
       for (int b = 0; b < S::FJ; ++b)
         vj[b] = __builtin_shufflevector(fj.read(tj, b, 0), fj.read(tj, b, 1), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
-      for (int a = 0; a < S::FI; ++a) {
+      for (int a = 0; a < FI; ++a) {
         const i32x8 vi =
             __builtin_shufflevector(fi.read(ti, a, 0), fi.read(ti, a, 1), 0, 1, 2, 3, 4, 5, 6, 7);
 #pragma unroll
@@ -282,26 +346,129 @@ __device__ __forceinline__ void multiply(lds_ptr lds, int steps, const LoadI &li
           for (int i = 0; i < 4; ++i) acc[a][b][i] = __builtin_fmaf(d[i], s, acc[a][b][i]);
         }
       }
+      stage = stage + 1 == S::NST ? 0 : stage + 1;
+    }
+  } else {
+    // Operands are read 64 contraction bytes ahead of the products that use them
+    // (half a step of 128 bytes, a whole one of 64), so that the matrix cores have work
+    // while the next operands leave LDS.
+    bf16x8 vi[2][FI], vj[2][S::FJ];
+    auto read = [&](int set, int half, int stage) {
+      lds_ptr ti = lds + stage * S::kStage, tj = ti + S::kBytesI;
+#pragma unroll
+      for (int b = 0; b < S::FJ; ++b) vj[set][b] = __builtin_bit_cast(bf16x8, fj.read(tj, b, half));
+#pragma unroll
+      for (int a = 0; a < FI; ++a) vi[set][a] = __builtin_bit_cast(bf16x8, fi.read(ti, a, half));
+    };
+    auto products = [&](int set) {
+#pragma unroll
+      for (int a = 0; a < FI; ++a)
+#pragma unroll
+        for (int b = 0; b < S::FJ; ++b)
+          acc[a][b] =
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(vj[set][b], vi[set][a], acc[a][b], 0, 0, 0);
+      // transposing reads come in twos
+      interleave<FI * (S::XI ? 2 : 1) + S::FJ * (S::XJ ? 2 : 1), FI * S::FJ>();
+    };
+    auto after = [](int stage) { return stage + 1 == S::NST ? 0 : stage + 1; };
+    wait_first<S>(younger);
+    issue_stage<S>(lds, S::NST - 1, S::NST - 1, steps, li, lj, sc);
+    read(0, 0, 0);
+    int stage = 0;
+    // the next stage has landed, and every wave has read the last of this one:
+    // its LDS takes the loads of step t + NST
+    auto turn_over = [&](int t) {
+      wait_and_meet<S::kLoads *(S::NST - 2)>();
+      issue_stage<S>(lds, t + S::NST, stage, steps, li, lj, sc);
+      stage = after(stage);
+    };
+    if constexpr (S::SB == 128) {
+      for (int t = 0; t < steps; ++t) {
+        read(1, 1, stage);
+        products(0);
+        turn_over(t);
+        read(0, 0, stage);
+        products(1);
+      }
     } else {
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        bf16x8 vi[S::FI], vj[S::FJ];
-#pragma unroll
-        for (int b = 0; b < S::FJ; ++b) vj[b] = __builtin_bit_cast(bf16x8, fj.read(tj, b, half));
-#pragma unroll
-        for (int a = 0; a < S::FI; ++a) vi[a] = __builtin_bit_cast(bf16x8, fi.read(ti, a, half));
-#pragma unroll
-        for (int a = 0; a < S::FI; ++a)
-#pragma unroll
-          for (int b = 0; b < S::FJ; ++b)
-            acc[a][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vj[b], vi[a], acc[a][b], 0, 0, 0);
+      // in twos: an odd count's last step multiplies zeros
+      for (int t = 0; t < steps; t += 2) {
+        turn_over(t);
+        read(1, 0, stage);
+        products(0);
+        turn_over(t + 1);
+        read(0, 0, stage);
+        products(1);
       }
     }
-    stage = stage + 1 == S::NST ? 0 : stage + 1;
   }
-  // the last stages' loads fetched nothing, but write LDS: drained before the
-  // workgroup gives it up
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  // The last stages' loads fetched nothing, but write LDS: drained here.  Past
+  // the barrier every wave's reads are done too, and LDS is free.
+  wait_and_meet<0>();
+}
+
+// ------------------------------------------------------------- epilogue ---
+
+// The lane number, as a value the compiler cannot compute ahead: what the
+// epilogue derives from it is then not kept in registers through the main loop.
+__device__ __forceinline__ int late_lane_id() {
+  int l = lane_id();
+  asm volatile("" : "+v"(l));
+  return l;
+}
+
+// A wave's results leave through LDS: block row a (16 rows of I) of COLS columns,
+// fp32, is written as the MFMA leaves it (4 columns of one row a lane) and read
+// back as 8 columns of one row a lane, so that global rows are read and written
+// in 16-byte pieces of whole lines.  The 16-byte chunk c of row r lies at c ^ r:
+// neither direction has bank conflicts.  One wave's region is its own: LDS
+// operations of a wave complete in order, so no barrier is needed.
+template <int COLS>
+struct Transpose {
+  static constexpr int kChunks = COLS / 4;
+  static constexpr int kBytes = 16 * COLS * 4;
+  static constexpr int kLanesPerRow = COLS / 8;
+  static constexpr int kPasses = 16 * kLanesPerRow / kWave;  // rows a lane gets back
+  static_assert(kPasses >= 1, "at least 32 columns");
+  lds_ptr base;
+  int l;  // the lane
+  __device__ __forceinline__ void put(int b, const f32x4 v) const {  // columns 16b .. 16b+15
+    const int r = l & 15, c = b * 4 + (l >> 4);
+    *(MOE_LDS f32x4 *)(base + r * COLS * 4 + ((c ^ r) & (kChunks - 1)) * 16) = v;
+  }
+  __device__ __forceinline__ int row(int pass) const {
+    return pass * (kWave / kLanesPerRow) + l / kLanesPerRow;
+  }
+  __device__ __forceinline__ int col() const { return l % kLanesPerRow * 8; }
+  __device__ __forceinline__ void get(int pass, float (&v)[8]) const {
+    const int r = row(pass), c = col() / 4;
+    const f32x4 a = *(MOE_LDS const f32x4 *)(base + r * COLS * 4 + ((c ^ r) & (kChunks - 1)) * 16);
+    const f32x4 b = *(MOE_LDS const f32x4 *)(base + r * COLS * 4 + (((c + 1) ^ r) & (kChunks - 1)) * 16);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[4 + i] = b[i];
+    }
+  }
+};
+
+__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8]) {
+  unpack8(*reinterpret_cast<const uint4 *>(p), v);
+}
+__device__ __forceinline__ bf16x8 round8(const float (&v)[8]) {
+  bf16x8 r;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) r[c] = static_cast<__bf16>(v[c]);
+  return r;
+}
+__device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
+  *reinterpret_cast<bf16x8 *>(p) = round8(v);
+}
+// Through a buffer resource, at byte `off`; kNowhere drops it.  Always one store of
+// the wave, whichever lanes have something to store (wait_first counts them).
+__device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0, 0);
 }
 
 // ---------------------------------------------------------- expert rows ---
@@ -325,53 +492,96 @@ __device__ __forceinline__ ExpertRows expert_rows(const int32_t *offsets, const 
 }
 
 struct RowTile {
-  int e;          // expert, -1: no tile for this workgroup
+  int e;             // expert, -1: no tile
   int start, count;  // its rows
-  int i0, j;      // first row of the tile in the expert, column tile
+  int i0, j;         // first row of the tile in the expert, column tile
 };
 
 // Row tiles are handed out expert by expert, groups of 8 row tiles at a time,
 // every column tile of a group before the next; neighbours in this order share
 // an expert's weights and rows.  Workgroups go round the 8 XCDs in turn, so an
-// XCD takes one contiguous run of the order: its L2 sees each panel once.
+// XCD takes one contiguous run of the order and its workgroups walk through it
+// side by side: its L2 sees each panel once.
 template <int BI>
-__device__ __forceinline__ RowTile find_row_tile(const int32_t *offsets, const int32_t *counts,
-                                                 int n_experts, int rows, int col_tiles) {
-  const int lane = lane_id();
-  const int per = (n_experts + kWave - 1) / kWave;  // experts a lane adds up
-  int mine = 0;
-  for (int u = 0; u < per; ++u) {
-    const int e = lane * per + u;
-    if (e < n_experts) mine += (expert_rows(offsets, counts, e, rows).count + BI - 1) / BI;
+struct RowTiles {
+  const int32_t *offsets, *counts;
+  int n_experts, rows, col_tiles;
+  int per;          // experts a lane adds up (at most 16)
+  int incl, mine;   // row tiles of the lanes up to this one, and of this one
+  int64_t total, chunk;
+
+  __device__ __forceinline__ void init(const int32_t *off, const int32_t *cnt, int experts, int nrows,
+                                       int cols) {
+    offsets = off;
+    counts = cnt;
+    n_experts = experts;
+    rows = nrows;
+    col_tiles = cols;
+    per = (n_experts + kWave - 1) / kWave;
+    mine = 0;
+    for (int u = 0; u < per; ++u) {
+      const int e = lane_id() * per + u;
+      if (e < n_experts) mine += (expert_rows(offsets, counts, e, rows).count + BI - 1) / BI;
+    }
+    incl = wave_incl_scan(mine);
+    total = static_cast<int64_t>(__builtin_amdgcn_readlane(incl, kWave - 1)) * col_tiles;
+    chunk = (total + 7) / 8;
   }
-  const int incl = wave_incl_scan(mine);
-  RowTile r;
-  r.e = -1;
-  const int64_t total = static_cast<int64_t>(__builtin_amdgcn_readlane(incl, kWave - 1)) * col_tiles;
-  const int64_t chunk = (total + 7) / 8;
-  const int64_t pos = blockIdx.x / 8, t = (blockIdx.x % 8) * chunk + pos;
-  if (pos >= chunk || t >= total) return r;
-  const uint64_t past = ballot(static_cast<int64_t>(incl) * col_tiles > t);
-  const int owner = __builtin_ctzll(past);
-  int before = __builtin_amdgcn_readlane(incl - mine, owner);
-  // the owner's experts, one per lane (per <= 16)
-  const int e = owner * per + lane;
-  ExpertRows x{0, 0};
-  if (lane < per && e < n_experts) x = expert_rows(offsets, counts, e, rows);
-  const int tiles = (x.count + BI - 1) / BI;
-  const int upto = wave_incl_scan(tiles);
-  const int who = __builtin_ctzll(ballot(static_cast<int64_t>(before + upto) * col_tiles > t));
-  r.e = owner * per + who;
-  r.start = __builtin_amdgcn_readlane(x.start, who);
-  r.count = __builtin_amdgcn_readlane(x.count, who);
-  const int ti = __builtin_amdgcn_readlane(tiles, who);
-  before += __builtin_amdgcn_readlane(upto - tiles, who);
-  const int q = static_cast<int>(t - static_cast<int64_t>(before) * col_tiles);
-  const int group = q / (8 * col_tiles), rest = q - group * 8 * col_tiles;
-  const int size = min(8, ti - group * 8);
-  r.j = rest / size;
-  r.i0 = (group * 8 + rest - r.j * size) * BI;
-  return r;
+
+  // The i-th tile of this workgroup.  An expert's last row tile holds fewer rows and
+  // takes less time; the workgroups change places from round to round, so that
+  // none meets such tiles every time.
+  __device__ __forceinline__ RowTile find(int i) const {
+    RowTile r;
+    r.e = -1;
+    const int each = gridDim.x / 8;  // workgroups of an XCD
+    const int64_t pos = static_cast<int64_t>(i) * each + (blockIdx.x / 8 + i) % each;
+    const int64_t t = (blockIdx.x % 8) * chunk + pos;
+    // (past the end in one round is past it in every later one)
+    if (pos >= chunk || t >= total) return r;
+    const int owner = __builtin_ctzll(ballot(static_cast<int64_t>(incl) * col_tiles > t));
+    int before = __builtin_amdgcn_readlane(incl - mine, owner);
+    // the owner's experts, one per lane
+    const int lane = lane_id(), e = owner * per + lane;
+    ExpertRows x{0, 0};
+    if (lane < per && e < n_experts) x = expert_rows(offsets, counts, e, rows);
+    const int tiles = (x.count + BI - 1) / BI;
+    const int upto = wave_incl_scan(tiles);
+    const int who = __builtin_ctzll(ballot(static_cast<int64_t>(before + upto) * col_tiles > t));
+    r.e = owner * per + who;
+    r.start = __builtin_amdgcn_readlane(x.start, who);
+    r.count = __builtin_amdgcn_readlane(x.count, who);
+    const int ti = __builtin_amdgcn_readlane(tiles, who);
+    before += __builtin_amdgcn_readlane(upto - tiles, who);
+    const int q = static_cast<int>(t - static_cast<int64_t>(before) * col_tiles);
+    const int group = q / (8 * col_tiles), rest = q - group * 8 * col_tiles;
+    const int size = min(8, ti - group * 8);
+    r.j = rest / size;
+    r.i0 = (group * 8 + rest - r.j * size) * BI;
+    return r;
+  }
+};
+
+// f(integral_constant<int, FI>) with the blocks of I that each wave needs for a tile
+// of `rows` rows, in quarters of all of them.
+template <class S, class F>
+__device__ __forceinline__ void with_blocks(int rows, F f) {
+  if constexpr (S::FI % 4 == 0) {
+    const int quarters = (rows + S::BI / 4 - 1) / (S::BI / 4);
+    if (quarters == 1) return f(std::integral_constant<int, S::FI / 4>());
+    if (quarters == 2) return f(std::integral_constant<int, S::FI / 2>());
+    if (quarters == 3) return f(std::integral_constant<int, S::FI / 4 * 3>());
+  }
+  f(std::integral_constant<int, S::FI>());
+}
+
+constexpr int kComputeUnits = 256;
+
+// Workgroups of a launch whose workgroups take tile after tile: at most
+// `resident` a compute unit, a multiple of the 8 XCDs.
+inline uint32_t tile_grid(int64_t tiles, int resident) {
+  const int64_t most = static_cast<int64_t>(kComputeUnits) * resident;
+  return static_cast<uint32_t>(((tiles < most ? tiles : most) + 7) / 8 * 8);
 }
 
 // Workgroups that cover every row tile of any routing of at most `pairs` rows.
@@ -383,7 +593,7 @@ inline int64_t row_tile_bound(int64_t pairs, int n_experts) {
 
 // ---------------------------------------------------------- activations ---
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // value and slope of an activation (a moe_act)
 template <int ACT>
