@@ -127,12 +127,9 @@ struct ProductArgs {
 template <class S, int FI>
 __device__ __forceinline__ int store_tile(lds_ptr lds, const f32x4 (&acc)[FI][S::FJ], uint16_t *out, int ld,
                                           int rows, int cols) {
-  constexpr int kCols = S::BJ / S::WJ;
-  static_assert(S::WI * S::WJ * Transpose<kCols>::kBytes <= S::kStage, "a region for each wave");
   const Wave<S> w = this_wave<S>();
-  const Transpose<kCols> turn{lds + (S::NST - 1) * S::kStage + wave_id() * Transpose<kCols>::kBytes,
-                              late_lane_id()};
-  const int col = w.wj * kCols + turn.col();
+  const auto turn = Transpose<S::kWaveCols>::template make<S>(lds, late_lane_id());
+  const int col = w.wj * S::kWaveCols + turn.col();
   const auto r = buffer_rsrc(out, kRecords);
 #pragma unroll
   for (int a = 0; a < FI; ++a) {
@@ -148,44 +145,49 @@ __device__ __forceinline__ int store_tile(lds_ptr lds, const f32x4 (&acc)[FI][S:
     }
     __builtin_amdgcn_wave_barrier();
   }
-  return FI * Transpose<kCols>::kPasses;
+  return FI * turn.kPasses;
 }
 
 template <class S>
 __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dx_kernel(ProductArgs g) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
   lds_ptr lds = (lds_ptr)smem;
-  const int row_bytes = g.n * 2, steps = (g.n + S::kStepRows - 1) / S::kStepRows;
   RowTiles<S::BI> order;
   order.init(g.offsets, g.counts, g.n_experts, g.rows, g.col_tiles);
-  AlongLoader<S, S::LI> li;
-  AcrossLoader<S, S::BJ, S::LJ> lj;
-  auto begin = [&](const RowTile &t) {
-    const int j0 = t.j * S::BJ;
-    li.init(g.dz + (static_cast<int64_t>(t.start) + t.i0) * g.n, row_bytes, [&](int r) {
-      return r < S::BI && t.i0 + r < t.count ? static_cast<uint32_t>(r * row_bytes) : kNowhere;
-    });
-    lj.init(g.w + static_cast<int64_t>(t.e) * g.n * g.k + j0, static_cast<int64_t>(g.k) * 2, g.n, g.k - j0);
-    start<S>(lds, steps, li, lj, NoScales());
-  };
   RowTile t = order.find(0);
   if (t.e < 0) return;
-  begin(t);
-  RowTile next;
-  int younger = 0;  // stores after the tile's first loads
+  Feed<S, Along<S, S::LI, SameRow>, Across<S, S::BJ, S::LJ>, NoScaleLanes> feed;
+  feed.i.init(g.n * 2);
+  feed.j.init(g.k * 2);
+  auto source = [&](const RowTile &r) {
+    Source s = kNoSource;
+    if (r.e < 0) return s;
+    const int j0 = r.j * S::BJ;
+    s.i = {reinterpret_cast<const char *>(g.dz + (static_cast<int64_t>(r.start) + r.i0) * g.n),
+           min(r.count - r.i0, S::BI) * g.n * 2, 0};
+    s.j = {reinterpret_cast<const char *>(g.w + static_cast<int64_t>(r.e) * g.n * g.k + j0), g.n, j0 * 2};
+    s.steps = (g.n + kStepRows - 1) / kStepRows;
+    return s;
+  };
+  Source cur = source(t), following;
+  start<S>(lds, feed, cur);
+  Progress at;
   auto one_tile = [&](auto blocks) {
     constexpr int FI = decltype(blocks)::value;
     f32x4 acc[FI][S::FJ];
-    multiply<S, FI>(lds, steps, li, lj, NoScales(), [](int) { return 0; }, younger, acc);
-    if (next.e >= 0) begin(next);
-    younger = store_tile<S, FI>(lds, acc, g.out + (static_cast<int64_t>(t.start) + t.i0) * g.k + t.j * S::BJ, g.k,
-                      t.count - t.i0, g.k - t.j * S::BJ);
+    multiply<S, FI>(lds, feed, cur, following, at, [](int) { return 0; }, acc);
+    at.younger = store_tile<S, FI>(
+        lds, acc, g.out + (static_cast<int64_t>(t.start) + t.i0) * g.k + t.j * S::BJ, g.k, t.count - t.i0,
+        g.k - t.j * S::BJ);
   };
   for (int n = 1; t.e >= 0; ++n) {
-    next = order.find(n);
+    const RowTile next = order.find(n);
+    following = source(next);
     with_blocks<S>(t.count - t.i0, one_tile);
     t = next;
+    cur = following;
   }
+  wait_and_meet<0>();  // loads past the last tile fetch nothing, but write LDS
 }
 
 // ---- dw = dz^T x -----------------------------------------------------------------
@@ -199,13 +201,11 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
   __shared__ __align__(1024) char smem[S::kLdsBytes];
   lds_ptr lds = (lds_ptr)smem;
   const int chunk = (total + 7) / 8, per = row_tiles * g.col_tiles;
-  AcrossLoader<S, S::BI, S::LI> li;
-  AcrossLoader<S, S::BJ, S::LJ> lj;
   struct Tile {
-    int e, i0, j0, steps;
+    int e, i0, j0;
   };
   auto find = [&](int n) {
-    Tile t{-1, 0, 0, 0};
+    Tile t{-1, 0, 0};
     const int64_t pos = blockIdx.x / 8 + static_cast<int64_t>(n) * (gridDim.x / 8);
     const int64_t id = (blockIdx.x % 8) * static_cast<int64_t>(chunk) + pos;
     if (pos >= chunk || id >= total) return t;
@@ -217,28 +217,36 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
     t.i0 = (group * 8 + rest % size) * S::BI;
     return t;
   };
-  auto begin = [&](Tile &t) {
-    const ExpertRows r = expert_rows(g.offsets, g.counts, t.e, g.rows);
-    t.steps = (r.count + S::kStepRows - 1) / S::kStepRows;
-    li.init(g.dz + static_cast<int64_t>(r.start) * g.n + t.i0, static_cast<int64_t>(g.n) * 2, r.count,
-            g.n - t.i0);
-    lj.init(g.x + static_cast<int64_t>(r.start) * g.k + t.j0, static_cast<int64_t>(g.k) * 2, r.count,
-            g.k - t.j0);
-    start<S>(lds, t.steps, li, lj, NoScales());
-  };
   Tile t = find(0);
   if (t.e < 0) return;
-  begin(t);
-  int younger = 0;  // stores after the tile's first loads
+  Feed<S, Across<S, S::BI, S::LI>, Across<S, S::BJ, S::LJ>, NoScaleLanes> feed;
+  feed.i.init(g.n * 2);
+  feed.j.init(g.k * 2);
+  auto source = [&](const Tile &r) {
+    Source s = kNoSource;
+    if (r.e < 0) return s;
+    const ExpertRows rows = expert_rows(g.offsets, g.counts, r.e, g.rows);
+    s.i = {reinterpret_cast<const char *>(g.dz + static_cast<int64_t>(rows.start) * g.n + r.i0), rows.count,
+           r.i0 * 2};
+    s.j = {reinterpret_cast<const char *>(g.x + static_cast<int64_t>(rows.start) * g.k + r.j0), rows.count,
+           r.j0 * 2};
+    s.steps = (rows.count + kStepRows - 1) / kStepRows;
+    return s;
+  };
+  Source cur = source(t);
+  start<S>(lds, feed, cur);
+  Progress at;
   for (int n = 1; t.e >= 0; ++n) {
+    const Tile next = find(n);
+    const Source following = source(next);
     f32x4 acc[S::FI][S::FJ];
-    multiply<S, S::FI>(lds, t.steps, li, lj, NoScales(), [](int) { return 0; }, younger, acc);
-    Tile next = find(n);
-    if (next.e >= 0) begin(next);
-    younger = store_tile<S, S::FI>(lds, acc, g.out + (static_cast<int64_t>(t.e) * g.n + t.i0) * g.k + t.j0, g.k, g.n - t.i0,
-                  g.k - t.j0);
+    multiply<S, S::FI>(lds, feed, cur, following, at, [](int) { return 0; }, acc);
+    at.younger = store_tile<S, S::FI>(lds, acc, g.out + (static_cast<int64_t>(t.e) * g.n + t.i0) * g.k + t.j0,
+                                      g.k, g.n - t.i0, g.k - t.j0);
     t = next;
+    cur = following;
   }
+  wait_and_meet<0>();  // loads past the last tile fetch nothing, but write LDS
 }
 
 template <class S>
@@ -300,12 +308,12 @@ hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, co
   a.n = width;
   if (b.dx) {
     a.out = b.dx;
-    err = launch_dx<Shape<256, 256, 2, 4, 128, 2, false, true>>(a, pairs, stream);
+    err = launch_dx<Shape<256, 256, 2, 4, 2, false, true>>(a, pairs, stream);
     if (err != hipSuccess) return err;
   }
   if (b.dw) {
     a.out = b.dw;
-    err = launch_dw<Shape<256, 256, 2, 4, 128, 2, true, true>>(a, stream);
+    err = launch_dw<Shape<256, 256, 2, 4, 2, true, true>>(a, stream);
   }
   return err;
 }

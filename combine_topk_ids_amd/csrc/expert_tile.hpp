@@ -11,21 +11,25 @@
 // J is the MFMA's A operand and I its B operand, so that a lane ends with four
 // neighbouring j of one i: 8-byte stores of bf16, and one row scale per lane.
 //
-// Memory path.  A step covers SB = 64 or 128 bytes of the contraction (32 or 64
-// bf16, 128 E4M3 values).  Tiles go from global memory straight into LDS (16 bytes a
-// lane, no registers), NST stages deep: the loads of step t + NST - 1 are
-// issued before the products of step t, and one barrier a step both publishes
-// a stage and frees the one before it.  Such a load writes 64 consecutive 16-byte chunks of
-// LDS, so there is no padding against bank conflicts; instead a lane picks which
-// chunk of its row it fetches:
-//   along c:  rows of SB / 16 chunks, chunk c of row r at along_chunk(r, c):
-//             the 16-byte operand reads of 8 consecutive lanes (8 rows, one
-//             chunk index) then touch 8 different 16-byte bank groups;
+// Memory path.  A step covers 128 bytes of the contraction (64 bf16 or 128 E4M3
+// values).  Tiles go from global memory straight into LDS (16 bytes a lane, no
+// registers), NST stages deep.  A workgroup takes tile after tile, and the
+// loads run on across the tiles: the stage that a step has freed takes the loads
+// of the step NST later, the next tile's first steps at a tile's end, so that
+// memory is not idle while results leave.  One barrier a step both publishes a
+// stage and frees the one before it.  Such a load writes 64
+// consecutive 16-byte chunks of LDS, so there is no padding against bank conflicts;
+// instead a lane picks which chunk of its row it fetches:
+//   along c:  rows of 8 chunks, chunk c of row r at position c ^ (r & 7); the
+//             16-byte operand reads of 8 consecutive lanes (8 rows, one chunk
+//             index) then touch 8 different 16-byte bank groups;
 //   across c: rows of 16-column groups (32 bytes), group g of row r at
 //             g ^ f(r), f taking r's bits 0, 1, 3, 4: the 16 rows that one
 //             transposing read visits for one group then lie in different banks.
-// Rows, columns and contraction indices past an operand's end are loads past
-// the buffer resource: they fetch nothing and leave zeros in LDS.
+// (Counters: no bank conflict in any of the products.)
+// Where an operand ends, the buffer resource ends: loads past it fetch nothing and
+// leave zeros in LDS.  What a lane adds to the resource's base is the same for
+// every tile; a tile is a few scalars.
 #pragma once
 
 #include <type_traits>
@@ -46,41 +50,43 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef MOE_LDS char *lds_ptr;
 
-// An offset past every buffer resource used here (their size is 2^31 - 1).
+constexpr int kStepBytes = 128;  // contraction bytes of one step
+constexpr int kStepRows = 64;    // contraction rows of one step, stored across c
+// An offset past every buffer resource used here (sizes stay below 2^31).
 constexpr uint32_t kNowhere = 0x80000000u;
 constexpr uint32_t kRecords = 0x7FFFFFFFu;
 
 // WI x WJ waves; each owns FI x FJ blocks of 16 x 16.  XI/XJ: the operand is
 // stored across c.  FP8: E4M3 codes (along c only) with block scales.
-template <int BI_, int BJ_, int WI_, int WJ_, int SB_, int NST_, bool XI_ = false, bool XJ_ = false,
+template <int BI_, int BJ_, int WI_, int WJ_, int NST_, bool XI_ = false, bool XJ_ = false,
           bool FP8_ = false>
 struct Shape {
   static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_;
-  static constexpr int SB = SB_;          // contraction bytes of one step
-  static constexpr int kStepRows = SB / 2;  // contraction rows of one step, stored across c
-  static constexpr int kChunks = SB / 16;   // 16-byte chunks of a step's row
-  
   static constexpr bool XI = XI_, XJ = XJ_, FP8 = FP8_;
   static constexpr int kThreads = WI * WJ * kWave;
   // at least two waves a SIMD: that also keeps the accumulators in the 256
   // registers that both operands and results of an MFMA can name (with more, the
   // compiler moves them to and from the accumulation registers in the loop)
-  static constexpr int kWavesPerSimd = BI * BJ / (WI * WJ) > 128 * 64 ? 1 : 2;
+  static constexpr int kWavesPerSimd = 2;
   static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
   // 16-byte loads a thread makes for an operand in a step; a tile smaller than one load
   // of every thread still gets a whole one (its spare rows are zeros)
-  static constexpr int loads(int b) { return (b * kChunks + kThreads - 1) / kThreads; }
+  static constexpr int loads(int b) { return (b * 8 + kThreads - 1) / kThreads; }
   static constexpr int LI = loads(BI), LJ = loads(BJ);
+  static constexpr int kLoadRows = kThreads / 8;  // tile rows between a thread's loads, along c
   static constexpr int kBytesI = LI * kThreads * 16, kBytesJ = LJ * kThreads * 16;
   static constexpr int kBytesScale = FP8 ? kThreads * 4 : 0;  // of each operand
   static constexpr int kStage = kBytesI + kBytesJ + 2 * kBytesScale;
-  static constexpr int kLdsBytes = NST * kStage;
+  // the results' way out: see Transpose.  FP8's larger stages leave room for half
+  static constexpr int kWaveCols = BJ / WJ;
+  static constexpr int kTurnCols = FP8 && kWaveCols > 32 ? 32 : kWaveCols;
+  static constexpr int kLdsBytes = NST * kStage + WI * WJ * 16 * kTurnCols * 4;
   // workgroups that a compute unit holds: LDS, and two waves a SIMD
   static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 4 * kWavesPerSimd / (WI * WJ);
   static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
-  static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // in flight per stage and wave
+  static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // of a wave and stage
   static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
-  static_assert(kLoads * (NST - 2) < 64, "the wait counter holds 63 loads");
+  static_assert(kLoads * (NST - 1) < 64, "the wait counter holds 63 loads");
   static_assert(kLdsBytes <= 160 * 1024, "LDS of a compute unit");
 };
 
@@ -93,43 +99,46 @@ __device__ __forceinline__ int wave_id() {
 __device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, lds_ptr to, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, static_cast<int>(off), 0, 0, 0);
 }
-
-// Position of chunk c of row r in an operand stored along c (and back).
-template <int SB>
-__device__ __forceinline__ int along_chunk(int r, int c) {
-  return SB == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
+__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, lds_ptr to, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 4, static_cast<int>(off), 0, 0, 0);
 }
 
-// Rows stored along c.  row_offset(r): byte offset from `base` of tile row r,
-// or kNowhere; row_bytes: bytes of a whole row (a multiple of 16).
-template <class S, int L>
-struct AlongLoader {
+// An operand of one tile (uniform).  Along c: `base` is its first row, `extent` the
+// bytes up to the end of its last.  Across c: `base` is the first column's place
+// in the first contraction row, `extent` the contraction rows, `skip` the bytes
+// before that place in a row.
+struct Operand {
   const char *base;
-  int row_bytes;
-  int chunk;         // byte offset in a step of the chunk this lane fetches
-  uint32_t off[L];
+  int extent, skip;
+};
+constexpr Operand kNoOperand{nullptr, 0, 0};
 
-  template <class F>
-  __device__ __forceinline__ void init(const void *b, int bytes, F row_offset) {
-    base = static_cast<const char *>(b);
+// Rows of `row_bytes` stored along c.  ROW(r) maps a tile row to a row of the
+// operand (it must satisfy ROW(a * kLoadRows + b) = ROW(a * kLoadRows) + ROW(b), b < kLoadRows).
+template <class S, int L, class ROW>
+struct Along {
+  ROW row;
+  int row_bytes, chunk;  // chunk: byte offset in a step of what this lane fetches
+  uint32_t off;
+
+  __device__ __forceinline__ void init(int bytes) {
     row_bytes = bytes;
-    const int tid = threadIdx.x;
-    chunk = along_chunk<S::SB>(tid / S::kChunks, tid % S::kChunks) * 16;
-#pragma unroll
-    for (int u = 0; u < L; ++u) {
-      const uint32_t o = row_offset((u * S::kThreads + tid) / S::kChunks);
-      off[u] = o == kNowhere ? kNowhere : o + chunk;
-    }
+    const int r = threadIdx.x / 8;
+    chunk = ((threadIdx.x & 7) ^ (r & 7)) * 16;
+    off = row(r) * bytes + chunk;
   }
-  __device__ __forceinline__ void issue(lds_ptr to, int step) const {
-    const int at = step * S::SB;
-    const auto r = buffer_rsrc(base + at, kRecords);
-    const bool ok = at + chunk < row_bytes;
+  __device__ __forceinline__ void issue(lds_ptr to, const Operand &o, int step) const {
+    const int at = step * kStepBytes;
+    const auto r = buffer_rsrc(o.base + at, max(o.extent - at, 0));
+    const uint32_t first = at + chunk < row_bytes ? off : kNowhere;  // the row's own end
     const int wave = wave_id();
 #pragma unroll
     for (int u = 0; u < L; ++u)
-      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16, ok ? off[u] : kNowhere);
+      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16, first + row(u * S::kLoadRows) * row_bytes);
   }
+};
+struct SameRow {
+  __device__ __forceinline__ uint32_t operator()(int r) const { return r; }
 };
 
 // The bank-spreading term of contraction row r in a tile of G 16-column groups.
@@ -138,81 +147,123 @@ __device__ __forceinline__ int group_mix(int r) {
   return ((r & 3) | (((r >> 3) & 3) << 2)) & (G - 1);
 }
 
-// Rows stored across c: `rows` contraction rows of `ld` bytes; B columns from
-// `base`, of which `cols` exist.
+// Contraction rows of `ld` bytes, B columns of them.  Columns past the operand's
+// are whatever follows in memory, inside the operand: they reach results past its
+// columns only, which are not stored.
 template <class S, int B, int L>
-struct AcrossLoader {
-  static constexpr int kChunks = B / 8;                 // 16-byte chunks of a tile row
-  static constexpr int kRowStep = S::kThreads / kChunks;  // rows between a thread's loads
-  static_assert(S::kStepRows * kChunks % S::kThreads == 0, "whole loads");
-  const char *base;
-  int64_t ld;
-  int rows;
-  uint32_t off[L];
+struct Across {
+  static constexpr int kChunks = B / 8;                   // 16-byte chunks of a tile row
+  static constexpr int kRows = S::kThreads / kChunks;     // rows between a thread's loads
+  static_assert(kStepRows * kChunks == L * S::kThreads && kRows % 16 == 0, "whole loads");
+  int ld;
+  uint32_t off[2];  // of the even and of the odd loads, within their rows
 
-  __device__ __forceinline__ void init(const void *b, int64_t row_bytes, int nrows, int cols) {
-    base = static_cast<const char *>(b);
+  __device__ __forceinline__ void init(int row_bytes) {
     ld = row_bytes;
-    rows = nrows;
-    const int ch = threadIdx.x % kChunks, r0 = threadIdx.x / kChunks;
+    const int ch = threadIdx.x % kChunks, r = threadIdx.x / kChunks;
 #pragma unroll
-    for (int u = 0; u < L; ++u) {
-      const int r = u * kRowStep + r0;
-      const int col = ((ch >> 1) ^ group_mix<B / 16>(r)) * 16 + (ch & 1) * 8;
-      off[u] = col < cols ? static_cast<uint32_t>(r * static_cast<int>(ld) + col * 2) : kNowhere;
-    }
+    for (int u = 0; u < 2; ++u)
+      off[u] = r * ld + ((ch >> 1) ^ group_mix<B / 16>(u * kRows + r)) * 32 + (ch & 1) * 16;
   }
-  __device__ __forceinline__ void issue(lds_ptr to, int step) const {
-    const auto r = buffer_rsrc(base + step * S::kStepRows * ld, kRecords);
-    const int left = rows - step * S::kStepRows - static_cast<int>(threadIdx.x) / kChunks;
+  __device__ __forceinline__ void issue(lds_ptr to, const Operand &o, int step) const {
+    const int left = min(max(o.extent - step * kStepRows, 0), kStepRows);
+    const auto r = buffer_rsrc(o.base + static_cast<int64_t>(step) * kStepRows * ld, max(left * ld - o.skip, 0));
     const int wave = wave_id();
 #pragma unroll
     for (int u = 0; u < L; ++u)
-      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16,
-                 u * kRowStep < left ? off[u] : kNowhere);
+      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16, off[u & 1] + u * kRows * ld);
   }
 };
 
 // Block scales of an FP8 step: thread r fetches the scale of tile row r, and
-// that of the weights' block r of the tile.
-struct ScaleLoader {
-  const float *rows, *weights;
-  uint32_t row_off, weight_off;  // bytes, of step 0
-  template <class S>
-  __device__ __forceinline__ void issue(lds_ptr to, int step, int steps) const {
-    const bool ok = step < steps;
+// that of the weights' block r of the tile, `blocks` scales a row.
+struct Scales {
+  const float *base;
+  int rows;  // scale rows from base on
+};
+template <class S>
+struct ScaleLanes {
+  int blocks;
+  uint32_t row_off, weight_off;
+  // weight_row: scale row of the weights' block that this thread fetches, relative to
+  // the tile's first, or kNowhere
+  __device__ __forceinline__ void init(int n, uint32_t weight_row) {
+    blocks = n;
+    row_off = threadIdx.x < S::BI ? threadIdx.x * n * 4 : kNowhere;
+    weight_off = weight_row == kNowhere ? kNowhere : weight_row * n * 4;
+  }
+  __device__ __forceinline__ void issue(lds_ptr to, const Scales &x, const Scales &w, int step) const {
     to += wave_id() * kWave * 4;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(rows + step, kRecords), (MOE_LDS void *)to, 4,
-                                             static_cast<int>(ok ? row_off : kNowhere), 0, 0, 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(weights + step, kRecords),
-                                             (MOE_LDS void *)(to + S::kBytesScale), 4,
-                                             static_cast<int>(ok ? weight_off : kNowhere), 0, 0, 0);
+    load_lds4(buffer_rsrc(x.base + step, bytes(x, step)), to, row_off);
+    load_lds4(buffer_rsrc(w.base + step, bytes(w, step)), to + S::kBytesScale, weight_off);
+  }
+  // left from the step's scales on; none past the last step, or of no tile
+  __device__ __forceinline__ uint32_t bytes(const Scales &s, int step) const {
+    return step < blocks ? max(s.rows * blocks - step, 0) * 4 : 0;
   }
 };
-struct NoScales {};
+struct NoScaleLanes {};  // bf16
+
+// What a tile is fed from (uniform), and its steps.
+struct Source {
+  Operand i, j;
+  Scales x, w;
+  int steps;
+};
+constexpr Source kNoSource{kNoOperand, kNoOperand, {nullptr, 0}, {nullptr, 0}, 0};
+
+// a or b, field by field (a choice between two whole ones would live in memory).
+__device__ __forceinline__ Operand either(bool c, const Operand &a, const Operand &b) {
+  return {c ? a.base : b.base, c ? a.extent : b.extent, c ? a.skip : b.skip};
+}
+template <bool FP8>
+__device__ __forceinline__ Source either(bool c, const Source &a, const Source &b) {
+  Source s = kNoSource;
+  s.i = either(c, a.i, b.i);
+  s.j = either(c, a.j, b.j);
+  if constexpr (FP8) {
+    s.x = {c ? a.x.base : b.x.base, c ? a.x.rows : b.x.rows};
+    s.w = {c ? a.w.base : b.w.base, c ? a.w.rows : b.w.rows};
+  }
+  return s;
+}
+
+// A launch's lanes.
+template <class S, class LI, class LJ, class LS>
+struct Feed {
+  LI i;
+  LJ j;
+  LS s;
+  __device__ __forceinline__ void issue(lds_ptr lds, int stage, const Source &src, int step) const {
+    lds_ptr to = lds + stage * S::kStage;
+    i.issue(to, src.i, step);
+    j.issue(to + S::kBytesI, src.j, step);
+    if constexpr (S::FP8) s.issue(to + S::kBytesI + S::kBytesJ, src.x, src.w, step);
+  }
+};
 
 // ------------------------------------------------------------- operands ---
 
 // Where a lane finds its part of its wave's 16-row blocks in a stage: block b of
 // the wave is block first + b * STRIDE of the tile.
-template <int F, int B, int SB, int STRIDE, bool X>
+template <int F, int B, int STRIDE, bool X>
 struct Fragments;
 
-template <int F, int B, int SB, int STRIDE>
-struct Fragments<F, B, SB, STRIDE, false> {
+template <int F, int B, int STRIDE>
+struct Fragments<F, B, STRIDE, false> {
   int at[2];  // contraction halves of the step
   __device__ __forceinline__ void init(int first_block) {
     const int l = lane_id();
-    at[0] = first_block * 16 * SB + (l & 15) * SB + along_chunk<SB>(l & 15, l >> 4) * 16;
+    at[0] = (first_block * 16 + (l & 15)) * kStepBytes + (((l >> 4) ^ (l & 7)) * 16);
     at[1] = at[0] ^ 64;
   }
   __device__ __forceinline__ i32x4 read(lds_ptr t, int b, int half) const {
-    return *(MOE_LDS const i32x4 *)(t + at[half] + b * STRIDE * 16 * SB);
+    return *(MOE_LDS const i32x4 *)(t + at[half] + b * STRIDE * 16 * kStepBytes);
   }
 };
 
-template <int F, int B, int SB, int STRIDE>
-struct Fragments<F, B, SB, STRIDE, true> {
+template <int F, int B, int STRIDE>
+struct Fragments<F, B, STRIDE, true> {
   int at[F];
   __device__ __forceinline__ void init(int first_block) {
     const int l = lane_id(), q = l >> 4, r = q * 8 + ((l >> 2) & 3);
@@ -235,7 +286,7 @@ struct Fragments<F, B, SB, STRIDE, true> {
 
 template <int N>
 __device__ __forceinline__ void wait_and_meet() {
-  // this wave's loads of the stage have landed and its LDS reads are done;
+  // at most N of this wave's loads are outstanding and its LDS reads are done;
   // past the barrier that holds for every wave
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
@@ -266,47 +317,42 @@ __device__ __forceinline__ Wave<S> this_wave() {
   return {w / S::WJ, w % S::WJ};
 }
 
-template <class S, class LoadI, class LoadJ, class Scales>
-__device__ __forceinline__ void issue_stage(lds_ptr lds, int step, int stage, int steps, const LoadI &li,
-                                            const LoadJ &lj, const Scales &sc) {
-  lds_ptr to = lds + stage * S::kStage;
-  li.issue(to, step);
-  lj.issue(to + S::kBytesI, step);
-  if constexpr (S::FP8) sc.template issue<S>(to + S::kBytesI + S::kBytesJ, step, steps);
-}
+// Where a wave stands between tiles.
+struct Progress {
+  int stage = 0;    // of the next tile's first step
+  int younger = 0;  // stores it has issued after the next tile's first loads
+};
 
-// The loads of a tile's first NST - 1 steps, into stages 0 .. NST - 2.
-template <class S, class LoadI, class LoadJ, class Scales>
-__device__ __forceinline__ void start(lds_ptr lds, int steps, const LoadI &li, const LoadJ &lj,
-                                      const Scales &sc) {
+// The loads of the first tile's first NST steps.
+template <class S, class F>
+__device__ __forceinline__ void start(lds_ptr lds, const F &feed, const Source &src) {
 #pragma unroll
-  for (int s = 0; s < S::NST - 1; ++s) issue_stage<S>(lds, s, s, steps, li, lj, sc);
+  for (int s = 0; s < S::NST; ++s) feed.issue(lds, s, src, s);
 }
 
-// The first wait of a tile: start()'s loads are older than the `younger` stores
-// with which the wave let the last tile go, and those need not be waited for.
-// (The counter runs down in the order of issue; a smaller count waits longer.)
-template <class S>
-__device__ __forceinline__ void wait_first(int younger) {
-  constexpr int kLater = S::kLoads * (S::NST - 2);
-  if (younger >= 16)
-    wait_and_meet<kLater + 16 < 64 ? kLater + 16 : 63>();
-  else if (younger >= 8)
-    wait_and_meet<kLater + 8 < 64 ? kLater + 8 : 63>();
+// Waits until at most N of this wave's loads, and the stores behind them, are
+// outstanding, then for the other waves.  (The counter runs down in the order of
+// issue, so a smaller count waits longer and is always safe.)
+template <int N>
+__device__ __forceinline__ void wait_behind(int stores) {
+  if (stores >= 16)
+    wait_and_meet<(N + 16 < 63 ? N + 16 : 63)>();
+  else if (stores >= 8)
+    wait_and_meet<(N + 8 < 63 ? N + 8 : 63)>();
   else
-    wait_and_meet<kLater>();
+    wait_and_meet<N>();
 }
 
-// acc[a][b] = the products of `steps` steps after start(), for the wave's first FI
-// blocks of I.  younger: see wait_first.  scale_j(b): index of the weights' scale
-// of block b in the stage's scale row (FP8 only).
-template <class S, int FI, class LoadI, class LoadJ, class Scales, class ScaleJ>
-__device__ __forceinline__ void multiply(lds_ptr lds, int steps, const LoadI &li, const LoadJ &lj,
-                                         const Scales &sc, ScaleJ scale_j, int younger,
-                                         f32x4 (&acc)[FI][S::FJ]) {
+// acc[a][b] = the products of cur's steps, for the wave's first FI blocks of I,
+// while the loads run on into `next`.  On entry the loads of cur's first NST steps
+// have been issued; on return those of next's.  scale_j(b): place of block b's
+// scale among the stage's weight scales (FP8 only).
+template <class S, int FI, class F, class ScaleJ>
+__device__ __forceinline__ void multiply(lds_ptr lds, const F &feed, const Source &cur, const Source &next,
+                                         Progress &at, ScaleJ scale_j, f32x4 (&acc)[FI][S::FJ]) {
   const Wave<S> w = this_wave<S>();
-  Fragments<FI, S::BI, S::SB, S::WI, S::XI> fi;
-  Fragments<S::FJ, S::BJ, S::SB, 1, S::XJ> fj;
+  Fragments<FI, S::BI, S::WI, S::XI> fi;
+  Fragments<S::FJ, S::BJ, 1, S::XJ> fj;
   fi.init(w.wi);
   fj.init(w.wj * S::FJ);
 #pragma unroll
@@ -314,97 +360,108 @@ __device__ __forceinline__ void multiply(lds_ptr lds, int steps, const LoadI &li
 #pragma unroll
     for (int b = 0; b < S::FJ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
+  // (a shorter tile goes through NST steps all the same, of zeros)
+  const int steps = max(cur.steps, S::NST);
+  int stage = at.stage;
+  // The next step's stage has landed, and every wave has read the last of this
+  // one's, which takes the loads of step t + NST.
+  auto turn_over = [&](int t) {
+    wait_behind<S::kLoads *(S::NST - 2)>(t < S::NST - 1 ? at.younger : 0);
+    const int s = t + S::NST;
+    const bool mine = s < steps;
+    feed.issue(lds, stage, either<S::FP8>(mine, cur, next), mine ? s : s - steps);
+    stage = stage + 1 == S::NST ? 0 : stage + 1;
+  };
+  wait_behind<S::kLoads *(S::NST - 1)>(at.younger);
+
   if constexpr (S::FP8) {
-    int stage = 0;
-    for (int t = 0; t < steps; ++t) {
-      wait_first<S>(t == 0 ? younger : 0);
-      // the stage that every wave has just finished reading
-      issue_stage<S>(lds, t + S::NST - 1, stage == 0 ? S::NST - 1 : stage - 1, steps, li, lj, sc);
-      lds_ptr ti = lds + stage * S::kStage, tj = ti + S::kBytesI;
-      lds_ptr ts = tj + S::kBytesJ;
-      float si[FI], sj[S::FJ];
+    // In phases of up to two blocks of I: a phase's products run while the next
+    // phase's operands are read, the next step's first ones in the last phase.
+    constexpr int kPair = FI % 2 == 0 ? 2 : 1, kPhases = FI / kPair;
+    i32x8 vi[2][kPair], vj[2][S::FJ];
+    float si[2][kPair], sj[2][S::FJ];
+    auto read_i = [&](int set, int phase) {
+      lds_ptr ti = lds + stage * S::kStage, ts = ti + S::kBytesI + S::kBytesJ;
 #pragma unroll
-      for (int a = 0; a < FI; ++a)
-        si[a] = *(MOE_LDS const float *)(ts + ((w.wi + a * S::WI) * 16 + (lane_id() & 15)) * 4);
-#pragma unroll
-      for (int b = 0; b < S::FJ; ++b)
-        sj[b] = *(MOE_LDS const float *)(ts + S::kBytesScale + scale_j(b) * 4);
-      i32x8 vj[S::FJ];
-#pragma unroll
-      for (int b = 0; b < S::FJ; ++b)
-        vj[b] = __builtin_shufflevector(fj.read(tj, b, 0), fj.read(tj, b, 1), 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-      for (int a = 0; a < FI; ++a) {
-        const i32x8 vi =
-            __builtin_shufflevector(fi.read(ti, a, 0), fi.read(ti, a, 1), 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-        for (int b = 0; b < S::FJ; ++b) {
-          const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              vj[b], vi, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-          const float s = si[a] * sj[b];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[a][b][i] = __builtin_fmaf(d[i], s, acc[a][b][i]);
-        }
+      for (int a = 0; a < kPair; ++a) {
+        const int blk = phase * kPair + a;
+        vi[set][a] =
+            __builtin_shufflevector(fi.read(ti, blk, 0), fi.read(ti, blk, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+        si[set][a] = *(MOE_LDS const float *)(ts + ((w.wi + blk * S::WI) * 16 + (lane_id() & 15)) * 4);
       }
-      stage = stage + 1 == S::NST ? 0 : stage + 1;
+    };
+    auto read_j = [&](int set) {
+      lds_ptr tj = lds + stage * S::kStage + S::kBytesI, ts = tj + S::kBytesJ + S::kBytesScale;
+#pragma unroll
+      for (int b = 0; b < S::FJ; ++b) {
+        vj[set][b] =
+            __builtin_shufflevector(fj.read(tj, b, 0), fj.read(tj, b, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+        sj[set][b] = *(MOE_LDS const float *)(ts + scale_j(b) * 4);
+      }
+    };
+    auto step = [&](int t, auto parity) {
+      constexpr int J = decltype(parity)::value;
+#pragma unroll
+      for (int ph = 0; ph < kPhases; ++ph) {
+        const int set = (ph + (kPhases % 2 ? J : 0)) & 1;
+        if (ph + 1 < kPhases) {
+          read_i(set ^ 1, ph + 1);
+        } else {
+          turn_over(t);
+          read_j(J ^ 1);
+          read_i(set ^ 1, 0);
+        }
+#pragma unroll
+        for (int a = 0; a < kPair; ++a)
+#pragma unroll
+          for (int b = 0; b < S::FJ; ++b) {
+            const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                vj[J][b], vi[set][a], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+            const float s = si[set][a] * sj[J][b];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[ph * kPair + a][b][i] = __builtin_fmaf(d[i], s, acc[ph * kPair + a][b][i]);
+          }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    read_j(0);
+    read_i(0, 0);
+    for (int t = 0; t < steps; t += 2) {
+      step(t, std::integral_constant<int, 0>());
+      if (t + 1 < steps) step(t + 1, std::integral_constant<int, 1>());
     }
   } else {
-    // Operands are read 64 contraction bytes ahead of the products that use them
-    // (half a step of 128 bytes, a whole one of 64), so that the matrix cores have work
-    // while the next operands leave LDS.
+    // Operands are read half a step ahead of the products that use them, so
+    // that the matrix cores have work while the next operands leave LDS.
     bf16x8 vi[2][FI], vj[2][S::FJ];
-    auto read = [&](int set, int half, int stage) {
+    auto read = [&](int half) {
       lds_ptr ti = lds + stage * S::kStage, tj = ti + S::kBytesI;
 #pragma unroll
-      for (int b = 0; b < S::FJ; ++b) vj[set][b] = __builtin_bit_cast(bf16x8, fj.read(tj, b, half));
+      for (int b = 0; b < S::FJ; ++b) vj[half][b] = __builtin_bit_cast(bf16x8, fj.read(tj, b, half));
 #pragma unroll
-      for (int a = 0; a < FI; ++a) vi[set][a] = __builtin_bit_cast(bf16x8, fi.read(ti, a, half));
+      for (int a = 0; a < FI; ++a) vi[half][a] = __builtin_bit_cast(bf16x8, fi.read(ti, a, half));
     };
-    auto products = [&](int set) {
+    auto products = [&](int half) {
 #pragma unroll
       for (int a = 0; a < FI; ++a)
 #pragma unroll
         for (int b = 0; b < S::FJ; ++b)
           acc[a][b] =
-              __builtin_amdgcn_mfma_f32_16x16x32_bf16(vj[set][b], vi[set][a], acc[a][b], 0, 0, 0);
+              __builtin_amdgcn_mfma_f32_16x16x32_bf16(vj[half][b], vi[half][a], acc[a][b], 0, 0, 0);
       // transposing reads come in twos
       interleave<FI * (S::XI ? 2 : 1) + S::FJ * (S::XJ ? 2 : 1), FI * S::FJ>();
     };
-    auto after = [](int stage) { return stage + 1 == S::NST ? 0 : stage + 1; };
-    wait_first<S>(younger);
-    issue_stage<S>(lds, S::NST - 1, S::NST - 1, steps, li, lj, sc);
-    read(0, 0, 0);
-    int stage = 0;
-    // the next stage has landed, and every wave has read the last of this one:
-    // its LDS takes the loads of step t + NST
-    auto turn_over = [&](int t) {
-      wait_and_meet<S::kLoads *(S::NST - 2)>();
-      issue_stage<S>(lds, t + S::NST, stage, steps, li, lj, sc);
-      stage = after(stage);
-    };
-    if constexpr (S::SB == 128) {
-      for (int t = 0; t < steps; ++t) {
-        read(1, 1, stage);
-        products(0);
-        turn_over(t);
-        read(0, 0, stage);
-        products(1);
-      }
-    } else {
-      // in twos: an odd count's last step multiplies zeros
-      for (int t = 0; t < steps; t += 2) {
-        turn_over(t);
-        read(1, 0, stage);
-        products(0);
-        turn_over(t + 1);
-        read(0, 0, stage);
-        products(1);
-      }
+    read(0);
+    for (int t = 0; t < steps; ++t) {
+      read(1);
+      products(0);
+      turn_over(t);
+      read(0);
+      products(1);
     }
   }
-  // The last stages' loads fetched nothing, but write LDS: drained here.  Past
-  // the barrier every wave's reads are done too, and LDS is free.
-  wait_and_meet<0>();
+  at.stage = stage;
 }
 
 // ------------------------------------------------------------- epilogue ---
@@ -425,6 +482,11 @@ __device__ __forceinline__ int late_lane_id() {
 // operations of a wave complete in order, so no barrier is needed.
 template <int COLS>
 struct Transpose {
+  // of this wave, behind the stages
+  template <class S>
+  __device__ __forceinline__ static Transpose make(lds_ptr lds, int lane) {
+    return {lds + S::NST * S::kStage + wave_id() * kBytes, lane};
+  }
   static constexpr int kChunks = COLS / 4;
   static constexpr int kBytes = 16 * COLS * 4;
   static constexpr int kLanesPerRow = COLS / 8;
@@ -465,7 +527,7 @@ __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
   *reinterpret_cast<bf16x8 *>(p) = round8(v);
 }
 // Through a buffer resource, at byte `off`; kNowhere drops it.  Always one store of
-// the wave, whichever lanes have something to store (wait_first counts them).
+// the wave, whichever lanes have something to store (wait_behind counts them).
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0, 0);
