@@ -225,7 +225,10 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
   auto source = [&](const Tile &r) {
     Source s = kNoSource;
     if (r.e < 0) return s;
-    const ExpertRows rows = expert_rows(g.offsets, g.counts, r.e, g.rows);
+    ExpertRows rows = expert_rows(g.offsets, g.counts, r.e, g.rows);
+    // the same in every lane: into scalar registers, where buffer resources live
+    rows.start = __builtin_amdgcn_readfirstlane(rows.start);
+    rows.count = __builtin_amdgcn_readfirstlane(rows.count);
     s.i = {reinterpret_cast<const char *>(g.dz + static_cast<int64_t>(rows.start) * g.n + r.i0), rows.count,
            r.i0 * 2};
     s.j = {reinterpret_cast<const char *>(g.x + static_cast<int64_t>(rows.start) * g.k + r.j0), rows.count,

@@ -96,11 +96,50 @@ __device__ __forceinline__ int wave_id() {
   return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
 }
 
-__device__ __forceinline__ void load_lds16(__amdgpu_buffer_rsrc_t r, lds_ptr to, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 16, static_cast<int>(off), 0, 0, 0);
+// A buffer resource in the four scalar registers that an instruction names.
+__device__ __forceinline__ i32x4 resource(const void *base, uint32_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(base);
+  return i32x4{__builtin_amdgcn_readfirstlane(static_cast<int>(a)),
+               __builtin_amdgcn_readfirstlane(static_cast<int>((a >> 32) & 0xFFFF)),
+               __builtin_amdgcn_readfirstlane(static_cast<int>(bytes)), kRawBufferConfig};
 }
-__device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t r, lds_ptr to, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (MOE_LDS void *)to, 4, static_cast<int>(off), 0, 0, 0);
+
+// Loads straight into LDS: lane l's 16 (or 4) bytes go to `to` + 16 l (4 l); load u's
+// to `to` + u * STRIDE.  Written as assembly because the compiler, which cannot
+// tell the stages apart, otherwise waits for every such load in flight before each
+// transposing read of LDS (seen in its output: the weights' gradient lost
+// its prefetch to that).  These loads have no register results; what waits for them
+// is wait_and_meet.  First line: scalars written by a vector instruction just before
+// need five cycles; after a write of m0, one.
+#define MOE_TO_LDS(N) "s_add_u32 m0, m0, %[stride]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o" #N "], %[r], 0 offen lds\n\t"
+#define MOE_TO_LDS_FIRST \
+  "s_nop 4\n\ts_mov_b32 m0, %[to]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o0], %[r], 0 offen lds\n\t"
+template <int STRIDE, int L>
+__device__ __forceinline__ void load_lds16(i32x4 r, lds_ptr to, const uint32_t (&o)[L]) {
+  static_assert(L == 1 || L == 2 || L == 4 || L == 8, "whole groups");
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<size_t>(to)));
+  if constexpr (L == 1)
+    asm volatile(MOE_TO_LDS_FIRST ::[o0] "v"(o[0]), [r] "s"(r), [to] "s"(at) : "memory", "m0", "scc");
+  if constexpr (L == 2)
+    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1)::[o0] "v"(o[0]), [o1] "v"(o[1]), [r] "s"(r), [to] "s"(at),
+                 [stride] "n"(STRIDE)
+                 : "memory", "m0", "scc");
+  if constexpr (L == 4)
+    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3)::[o0] "v"(o[0]), [o1] "v"(o[1]),
+                 [o2] "v"(o[2]), [o3] "v"(o[3]), [r] "s"(r), [to] "s"(at), [stride] "n"(STRIDE)
+                 : "memory", "m0", "scc");
+  if constexpr (L == 8)
+    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3) MOE_TO_LDS(4) MOE_TO_LDS(5)
+                     MOE_TO_LDS(6) MOE_TO_LDS(7)::[o0] "v"(o[0]), [o1] "v"(o[1]), [o2] "v"(o[2]),
+                 [o3] "v"(o[3]), [o4] "v"(o[4]), [o5] "v"(o[5]), [o6] "v"(o[6]), [o7] "v"(o[7]), [r] "s"(r),
+                 [to] "s"(at), [stride] "n"(STRIDE)
+                 : "memory", "m0", "scc");
+}
+__device__ __forceinline__ void load_lds4(i32x4 r, lds_ptr to, uint32_t o) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<size_t>(to)));
+  asm volatile("s_nop 4\n\ts_mov_b32 m0, %[to]\n\ts_nop 0\n\tbuffer_load_dword %[o], %[r], 0 offen lds" ::[o] "v"(o),
+               [r] "s"(r), [to] "s"(at)
+               : "memory", "m0");
 }
 
 // An operand of one tile (uniform).  Along c: `base` is its first row, `extent` the
@@ -129,12 +168,12 @@ struct Along {
   }
   __device__ __forceinline__ void issue(lds_ptr to, const Operand &o, int step) const {
     const int at = step * kStepBytes;
-    const auto r = buffer_rsrc(o.base + at, max(o.extent - at, 0));
     const uint32_t first = at + chunk < row_bytes ? off : kNowhere;  // the row's own end
-    const int wave = wave_id();
+    uint32_t place[L];
 #pragma unroll
-    for (int u = 0; u < L; ++u)
-      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16, first + row(u * S::kLoadRows) * row_bytes);
+    for (int u = 0; u < L; ++u) place[u] = first + row(u * S::kLoadRows) * row_bytes;
+    load_lds16<S::kThreads * 16>(resource(o.base + at, max(o.extent - at, 0)), to + wave_id() * kWave * 16,
+                                 place);
   }
 };
 struct SameRow {
@@ -167,11 +206,12 @@ struct Across {
   }
   __device__ __forceinline__ void issue(lds_ptr to, const Operand &o, int step) const {
     const int left = min(max(o.extent - step * kStepRows, 0), kStepRows);
-    const auto r = buffer_rsrc(o.base + static_cast<int64_t>(step) * kStepRows * ld, max(left * ld - o.skip, 0));
-    const int wave = wave_id();
+    uint32_t place[L];
 #pragma unroll
-    for (int u = 0; u < L; ++u)
-      load_lds16(r, to + (u * S::kThreads + wave * kWave) * 16, off[u & 1] + u * kRows * ld);
+    for (int u = 0; u < L; ++u) place[u] = off[u & 1] + u * kRows * ld;
+    load_lds16<S::kThreads * 16>(
+        resource(o.base + static_cast<int64_t>(step) * kStepRows * ld, max(left * ld - o.skip, 0)),
+        to + wave_id() * kWave * 16, place);
   }
 };
 
@@ -194,8 +234,8 @@ struct ScaleLanes {
   }
   __device__ __forceinline__ void issue(lds_ptr to, const Scales &x, const Scales &w, int step) const {
     to += wave_id() * kWave * 4;
-    load_lds4(buffer_rsrc(x.base + step, bytes(x, step)), to, row_off);
-    load_lds4(buffer_rsrc(w.base + step, bytes(w, step)), to + S::kBytesScale, weight_off);
+    load_lds4(resource(x.base + step, bytes(x, step)), to, row_off);
+    load_lds4(resource(w.base + step, bytes(w, step)), to + S::kBytesScale, weight_off);
   }
   // left from the step's scales on; none past the last step, or of no tile
   __device__ __forceinline__ uint32_t bytes(const Scales &s, int step) const {
