@@ -19,6 +19,7 @@ using namespace tile;
 constexpr int kChunkRows = 64;   // rows of one workgroup (and of one partial sum)
 constexpr int kSlabCols = 512;   // columns of a workgroup: 8 a lane
 constexpr int kWaves = 4;
+constexpr int kBatch = 4;
 
 struct GradArgs {
   const uint16_t *dy, *preact;
@@ -41,30 +42,43 @@ __global__ __launch_bounds__(kWaves *kWave) void grad_kernel(GradArgs g) {
   const bool live = col < g.n;
   float s0[8] = {}, s1[8] = {};
   const int end = min(t.count, t.i0 + kChunkRows);
-  for (int i = t.i0 + wave; live && i < end; i += kWaves) {
-    const int64_t row = static_cast<int64_t>(t.start) + i;
-    float d[8], z[8];
-    load8(g.dy + row * g.n + col, d);
-    if constexpr (GLU) {
-      float up[8];
-      load8(g.preact + row * g.width + col, z);
-      load8(g.preact + row * g.width + g.n + col, up);
+  // kBatch rows at a time: their loads are in flight together
+  for (int i = t.i0 + wave; live && i < end; i += kWaves * kBatch) {
+    uint4 rd[kBatch], rz[kBatch], ru[kBatch];
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        const float gate = z[c];
-        z[c] = d[c] * act_value<ACT>(gate);
-        d[c] = d[c] * up[c] * act_slope<ACT>(gate);
-        s1[c] += z[c];
-      }
-      store8(g.dz + row * g.width + g.n + col, z);
-    } else if constexpr (ACT != MOE_ACT_NONE) {
-      load8(g.preact + row * g.n + col, z);
-#pragma unroll
-      for (int c = 0; c < 8; ++c) d[c] *= act_slope<ACT>(z[c]);
+    for (int u = 0; u < kBatch; ++u) {
+      const int64_t row = static_cast<int64_t>(t.start) + min(i + u * kWaves, end - 1);
+      rd[u] = *reinterpret_cast<const uint4 *>(g.dy + row * g.n + col);
+      if (GLU || ACT != MOE_ACT_NONE) rz[u] = *reinterpret_cast<const uint4 *>(g.preact + row * g.width + col);
+      if (GLU) ru[u] = *reinterpret_cast<const uint4 *>(g.preact + row * g.width + g.n + col);
     }
-    if (GLU || ACT != MOE_ACT_NONE) store8(g.dz + row * g.width + col, d);
 #pragma unroll
-    for (int c = 0; c < 8; ++c) s0[c] += d[c];
+    for (int u = 0; u < kBatch; ++u) {
+      if (i + u * kWaves >= end) break;
+      const int64_t row = static_cast<int64_t>(t.start) + i + u * kWaves;
+      float d[8], z[8];
+      unpack8(rd[u], d);
+      if constexpr (GLU) {
+        float up[8];
+        unpack8(rz[u], z);
+        unpack8(ru[u], up);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          const float gate = z[c];
+          z[c] = d[c] * act_value<ACT>(gate);
+          d[c] = d[c] * up[c] * act_slope<ACT>(gate);
+          s1[c] += z[c];
+        }
+        store8(g.dz + row * g.width + g.n + col, z);
+      } else if constexpr (ACT != MOE_ACT_NONE) {
+        unpack8(rz[u], z);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) d[c] *= act_slope<ACT>(z[c]);
+      }
+      if (GLU || ACT != MOE_ACT_NONE) store8(g.dz + row * g.width + col, d);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) s0[c] += d[c];
+    }
   }
   if (!g.partial) return;
 #pragma unroll
@@ -271,6 +285,33 @@ hipError_t launch_dw(ProductArgs g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+hipError_t launch_dx_sized(const ProductArgs &g, int64_t pairs, hipStream_t stream) {
+  typedef Shape<256, 256, 2, 4, 2, false, true> Large;
+  typedef Shape<128, 128, 2, 2, 2, false, true> Middle;
+  typedef Shape<64, 128, 2, 2, 4, false, true> Small;
+  if (row_tile_bound<Large::BI>(pairs, g.n_experts) * col_tiles<Large::BJ>(g.k) >= kEnoughTiles)
+    return launch_dx<Large>(g, pairs, stream);
+  if (row_tile_bound<Middle::BI>(pairs, g.n_experts) * col_tiles<Middle::BJ>(g.k) >= kEnoughTiles)
+    return launch_dx<Middle>(g, pairs, stream);
+  return launch_dx<Small>(g, pairs, stream);
+}
+
+// (2N = K = 1024: 8 experts, 128 tiles of 256 x 256, 31.6 us, of 128 x 128, 22.3;
+// 16 experts, 256 tiles, 12.8 and 13.3; 2 experts with 2N = 512, K = 256 and 8192 rows,
+// 16 tiles of 128 x 128, 79.7, of 64 x 64, 49.5.)
+hipError_t launch_dw_sized(const ProductArgs &g, hipStream_t stream) {
+  typedef Shape<256, 256, 2, 4, 2, true, true> Large;
+  typedef Shape<128, 128, 2, 2, 2, true, true> Middle;
+  typedef Shape<64, 64, 2, 2, 6, true, true> Small;
+  auto tiles = [&](auto shape) {
+    typedef decltype(shape) S;
+    return g.n_experts * col_tiles<S::BI>(g.n) * col_tiles<S::BJ>(g.k);
+  };
+  if (tiles(Large()) >= kComputeUnits) return launch_dw<Large>(g, stream);
+  if (tiles(Middle()) >= kEnoughTiles) return launch_dw<Middle>(g, stream);
+  return launch_dw<Small>(g, stream);
+}
+
 }  // namespace
 
 hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, const moe_expert_op &op,
@@ -311,12 +352,12 @@ hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, co
   a.n = width;
   if (b.dx) {
     a.out = b.dx;
-    err = launch_dx<Shape<256, 256, 2, 4, 2, false, true>>(a, pairs, stream);
+    err = launch_dx_sized(a, pairs, stream);
     if (err != hipSuccess) return err;
   }
   if (b.dw) {
     a.out = b.dw;
-    err = launch_dw<Shape<256, 256, 2, 4, 2, true, true>>(a, stream);
+    err = launch_dw_sized(a, stream);
   }
   return err;
 }

@@ -181,33 +181,51 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void forward_kernel(
   wait_and_meet<0>();  // loads past the last tile fetch nothing, but write LDS
 }
 
+// resident: tile_grid's
 template <class S, bool GLU>
-hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream) {
+hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream, int resident = S::kResident) {
   constexpr int kCols = GLU ? S::BJ / 2 : S::BJ;
   g.col_tiles = (g.n + kCols - 1) / kCols;
   const int64_t tiles = row_tile_bound<S::BI>(pairs, g.n_experts) * g.col_tiles;
-  const uint32_t grid = tile_grid(tiles, S::kResident);
+  const uint32_t grid = tile_grid(tiles, resident);
   return with_act(act, [&](auto a) {
     forward_kernel<S, GLU, decltype(a)::value><<<grid, S::kThreads, 0, stream>>>(g);
     return hipGetLastError();
   });
 }
 
-// Which tile: by the rows an expert has on average, and by whether larger tiles would
-// leave compute units without work.
+// Which tile, by the rows an expert has on average and by whether larger tiles would
+// leave compute units without work.  Measured at K = 4096, F = 1024 (gated, 64
+// experts, top 6; us a call, bf16 unless FP8 is said):
+//   rows an expert    0.1     0.75    4      64     96    128    192
+//   16 x 64           21.2   115.5  187.1   420.6  586.1  748.8 1038.9
+//   128 x 128         54.0   145.0  181.9   192.6  205.8  310.8  315.8
+//   256 x 256         72.3   165.6  193.3   211.1  224.2  235.6  268.9
+// FP8 stays with 128 x 128: a 256 x 256 tile's sums, operands and block products
+// do not fit the registers.  With many rows its workgroups take one tile each, so that
+// tiles which share weights start together (K = 7168, F = 2048, 256 experts of
+// 256 rows: 3158 us against 4231 for workgroups that take tile after tile, whose
+// L2 misses were 22.9 GB against 15.2); with few the weights pass once in any order
+// (1295 against 1204 us at 4 rows).
 template <bool GLU, bool FP8>
 hipError_t launch_sized(const ForwardArgs &g, int64_t pairs, int act, hipStream_t stream) {
-#ifdef SHAPE
-  return launch<Shape<SHAPE, false, false, FP8>, GLU>(g, pairs, act, stream);
-#endif
   typedef Shape<16, 64, 1, 1, 6, false, false, FP8> Few;
+  typedef Shape<64, 128, 2, 2, 3, false, false, FP8> Low;
   typedef Shape<128, 128, 2, 2, 2, false, false, FP8> Some;
-  typedef Shape<256, 256, 2, 4, 2, false, false, FP8> Many;
   const int64_t used = pairs < g.n_experts ? pairs : g.n_experts, rows = (pairs + used - 1) / used;
-  const int64_t tiles = row_tile_bound<Some::BI>(pairs, g.n_experts) * ((g.n * (GLU ? 2 : 1) + 127) / 128);
+  const int wrows = g.n * (GLU ? 2 : 1);
+  const int64_t tiles = row_tile_bound<Some::BI>(pairs, g.n_experts) * col_tiles<Some::BJ>(wrows);
   if (rows <= 16 && tiles < 4 * kComputeUnits) return launch<Few, GLU>(g, pairs, act, stream);
-  if (rows > 112) return launch<Many, GLU>(g, pairs, act, stream);
-  return launch<Some, GLU>(g, pairs, act, stream);
+  if (tiles < kEnoughTiles) return launch<Low, GLU>(g, pairs, act, stream);
+  if (rows <= 112) return launch<Some, GLU>(g, pairs, act, stream);
+  if constexpr (FP8) {
+    return launch<Some, GLU>(g, pairs, act, stream, kAnyNumber);
+  } else {
+    typedef Shape<256, 256, 2, 4, 2> Many;
+    if (row_tile_bound<Many::BI>(pairs, g.n_experts) * col_tiles<Many::BJ>(wrows) < kEnoughTiles)
+      return launch<Some, GLU>(g, pairs, act, stream);
+    return launch<Many, GLU>(g, pairs, act, stream);
+  }
 }
 
 }  // namespace

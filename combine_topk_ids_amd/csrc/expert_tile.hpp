@@ -67,7 +67,8 @@ struct Shape {
   // at least two waves a SIMD: that also keeps the accumulators in the 256
   // registers that both operands and results of an MFMA can name (with more, the
   // compiler moves them to and from the accumulation registers in the loop)
-  static constexpr int kWavesPerSimd = 2;
+  // (a workgroup of one wave is held to fewer by its LDS)
+  static constexpr int kWavesPerSimd = WI * WJ >= 4 ? 2 : 1;
   static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
   // 16-byte loads a thread makes for an operand in a step; a tile smaller than one load
   // of every thread still gets a whole one (its spare rows are zeros)
@@ -82,7 +83,7 @@ struct Shape {
   static constexpr int kTurnCols = FP8 && kWaveCols > 32 ? 32 : kWaveCols;
   static constexpr int kLdsBytes = NST * kStage + WI * WJ * 16 * kTurnCols * 4;
   // workgroups that a compute unit holds: LDS, and two waves a SIMD
-  static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 4 * kWavesPerSimd / (WI * WJ);
+  static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (WI * WJ);
   static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
   static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // of a wave and stage
   static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
@@ -415,57 +416,50 @@ __device__ __forceinline__ void multiply(lds_ptr lds, const F &feed, const Sourc
   wait_behind<S::kLoads *(S::NST - 1)>(at.younger);
 
   if constexpr (S::FP8) {
-    // In phases of up to two blocks of I: a phase's products run while the next
-    // phase's operands are read, the next step's first ones in the last phase.
-    constexpr int kPair = FI % 2 == 0 ? 2 : 1, kPhases = FI / kPair;
-    i32x8 vi[2][kPair], vj[2][S::FJ];
-    float si[2][kPair], sj[2][S::FJ];
-    auto read_i = [&](int set, int phase) {
+    // A phase for each block of I: its products run while the next block's rows are
+    // read.  In a step's last phase each block of J makes way, after its product,
+    // for the next step's.  (Reading further ahead would not leave registers for
+    // 128 sums.)
+    i32x8 vi[2], vj[S::FJ];
+    float si[2], sj[S::FJ];
+    auto read_i = [&](int set, int blk) {
       lds_ptr ti = lds + stage * S::kStage, ts = ti + S::kBytesI + S::kBytesJ;
-#pragma unroll
-      for (int a = 0; a < kPair; ++a) {
-        const int blk = phase * kPair + a;
-        vi[set][a] =
-            __builtin_shufflevector(fi.read(ti, blk, 0), fi.read(ti, blk, 1), 0, 1, 2, 3, 4, 5, 6, 7);
-        si[set][a] = *(MOE_LDS const float *)(ts + ((w.wi + blk * S::WI) * 16 + (lane_id() & 15)) * 4);
-      }
+      vi[set] = __builtin_shufflevector(fi.read(ti, blk, 0), fi.read(ti, blk, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+      si[set] = *(MOE_LDS const float *)(ts + ((w.wi + blk * S::WI) * 16 + (lane_id() & 15)) * 4);
     };
-    auto read_j = [&](int set) {
+    auto read_j = [&](int b) {
       lds_ptr tj = lds + stage * S::kStage + S::kBytesI, ts = tj + S::kBytesJ + S::kBytesScale;
-#pragma unroll
-      for (int b = 0; b < S::FJ; ++b) {
-        vj[set][b] =
-            __builtin_shufflevector(fj.read(tj, b, 0), fj.read(tj, b, 1), 0, 1, 2, 3, 4, 5, 6, 7);
-        sj[set][b] = *(MOE_LDS const float *)(ts + scale_j(b) * 4);
-      }
+      vj[b] = __builtin_shufflevector(fj.read(tj, b, 0), fj.read(tj, b, 1), 0, 1, 2, 3, 4, 5, 6, 7);
+      sj[b] = *(MOE_LDS const float *)(ts + scale_j(b) * 4);
     };
-    auto step = [&](int t, auto parity) {
-      constexpr int J = decltype(parity)::value;
+    auto step = [&](int t, auto odd) {
 #pragma unroll
-      for (int ph = 0; ph < kPhases; ++ph) {
-        const int set = (ph + (kPhases % 2 ? J : 0)) & 1;
-        if (ph + 1 < kPhases) {
-          read_i(set ^ 1, ph + 1);
-        } else {
-          turn_over(t);
-          read_j(J ^ 1);
-          read_i(set ^ 1, 0);
-        }
+      for (int a = 0; a < FI; ++a) {
+        const int set = (a + (FI % 2 ? decltype(odd)::value : 0)) & 1;
+        const bool last = a + 1 == FI;
+        if (last) turn_over(t);
+        read_i(set ^ 1, last ? 0 : a + 1);
+        // the product of block b, then what that of b - 1 adds to its sum
+        f32x4 d[2];
+        float scale[2];
 #pragma unroll
-        for (int a = 0; a < kPair; ++a)
-#pragma unroll
-          for (int b = 0; b < S::FJ; ++b) {
-            const f32x4 d = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                vj[J][b], vi[set][a], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-            const float s = si[set][a] * sj[J][b];
+        for (int b = 0; b <= S::FJ; ++b) {
+          if (b < S::FJ) {
+            scale[b & 1] = si[set] * sj[b];
+            d[b & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                vj[b], vi[set], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+            if (last) read_j(b);
+          }
+          if (b > 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              acc[ph * kPair + a][b][i] = __builtin_fmaf(d[i], s, acc[ph * kPair + a][b][i]);
+              acc[a][b - 1][i] = __builtin_fmaf(d[(b - 1) & 1][i], scale[(b - 1) & 1], acc[a][b - 1][i]);
           }
-        __builtin_amdgcn_sched_barrier(0);
+        }
       }
     };
-    read_j(0);
+#pragma unroll
+    for (int b = 0; b < S::FJ; ++b) read_j(b);
     read_i(0, 0);
     for (int t = 0; t < steps; t += 2) {
       step(t, std::integral_constant<int, 0>());
@@ -679,8 +673,22 @@ __device__ __forceinline__ void with_blocks(int rows, F f) {
 
 constexpr int kComputeUnits = 256;
 
-// Workgroups of a launch whose workgroups take tile after tile: at most
-// `resident` a compute unit, a multiple of the 8 XCDs.
+// Tiles of B columns that cover n of them.
+template <int B>
+inline int64_t col_tiles(int n) {
+  return (n + B - 1) / B;
+}
+
+// Fewer tiles than this leave so many of the 256 compute units without work that
+// smaller tiles are faster, though each feeds the matrix cores less well.  (Rows'
+// gradient, K = 2N = 1024: 8 experts of 512 rows, 160 tiles of 256 x 256, 51.9 us, of
+// 128 x 128, 52.4; of 256 rows, 64 tiles, 46.3 against 23.4; of 128 rows, 127
+// tiles of 128 x 128, 22.5 against 16.8 of 64 x 128.)
+constexpr int kEnoughTiles = 128;
+
+// Workgroups of a launch: at most `resident` a compute unit, which then take tile
+// after tile, or as many as there are tiles (kAnyNumber); a multiple of the 8 XCDs.
+constexpr int kAnyNumber = 1 << 20;
 inline uint32_t tile_grid(int64_t tiles, int resident) {
   const int64_t most = static_cast<int64_t>(kComputeUnits) * resident;
   return static_cast<uint32_t>(((tiles < most ? tiles : most) + 7) / 8 * 8);
