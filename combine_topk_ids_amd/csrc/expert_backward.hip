@@ -134,13 +134,16 @@ struct ProductArgs {
   int n_experts, rows;
   int k, n;       // columns of x and of dz
   int col_tiles;
+  float *parts;   // dw's, where its rows are split
 };
 
 // Results of a wave, to a tile of rows x cols of `out`, whose rows have `ld`
 // columns.  Returns the wave's stores.
-template <class S, int FI>
-__device__ __forceinline__ int store_tile(lds_ptr lds, const f32x4 (&acc)[FI][S::FJ], uint16_t *out, int ld,
-                                          int rows, int cols) {
+// T: uint16_t (bf16, rounded here) or float.
+template <class S, int FI, class T>
+__device__ __forceinline__ int store_tile(lds_ptr lds, const f32x4 (&acc)[FI][S::FJ], T *out, int ld, int rows,
+                                          int cols) {
+  constexpr int kSize = sizeof(T);
   const Wave<S> w = this_wave<S>();
   const auto turn = Transpose<S::kWaveCols>::template make<S>(lds, late_lane_id());
   const int col = w.wj * S::kWaveCols + turn.col();
@@ -155,11 +158,15 @@ __device__ __forceinline__ int store_tile(lds_ptr lds, const f32x4 (&acc)[FI][S:
       const int i = (w.wi + a * S::WI) * 16 + turn.row(p);
       float v[8];
       turn.get(p, v);
-      store8(r, i < rows && col < cols ? static_cast<uint32_t>(i * ld + col) * 2 : kNowhere, v);
+      const uint32_t at = i < rows && col < cols ? static_cast<uint32_t>(i * ld + col) * kSize : kNowhere;
+      if constexpr (kSize == 2)
+        store8(r, at, v);
+      else
+        store8_f32(r, at, v);
     }
     __builtin_amdgcn_wave_barrier();
   }
-  return FI * turn.kPasses;
+  return FI * turn.kPasses * (kSize / 2);
 }
 
 template <class S>
@@ -209,20 +216,26 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dx_kernel(Produ
 // BI x BJ tiles of the experts' dw: the contraction runs over the expert's rows,
 // none of them for an expert without rows (its dw is zeros).  An XCD takes one
 // run of tiles, expert by expert: the expert's rows stay in its L2.
-template <class S>
-__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(ProductArgs g, int row_tiles,
-                                                                           int total) {
+// PARTS: the rows of an expert are split into `parts` runs of whole steps, whose
+// sums go to the workspace [parts][E][n][k] as fp32 and are added by join_kernel.
+template <class S, bool PARTS>
+__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(ProductArgs g, int row_tiles, int total,
+                                                                           int parts) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
   lds_ptr lds = (lds_ptr)smem;
   const int chunk = (total + 7) / 8, per = row_tiles * g.col_tiles;
   struct Tile {
-    int e, i0, j0;
+    int e, i0, j0, part;
   };
   auto find = [&](int n) {
-    Tile t{-1, 0, 0};
+    Tile t{-1, 0, 0, 0};
     const int64_t pos = blockIdx.x / 8 + static_cast<int64_t>(n) * (gridDim.x / 8);
-    const int64_t id = (blockIdx.x % 8) * static_cast<int64_t>(chunk) + pos;
+    int64_t id = (blockIdx.x % 8) * static_cast<int64_t>(chunk) + pos;
     if (pos >= chunk || id >= total) return t;
+    if constexpr (PARTS) {
+      t.part = static_cast<int>(id % parts);
+      id /= parts;
+    }
     t.e = static_cast<int>(id / per);
     const int q = static_cast<int>(id - static_cast<int64_t>(t.e) * per);
     const int group = q / (8 * g.col_tiles), rest = q - group * 8 * g.col_tiles;
@@ -240,6 +253,12 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
     Source s = kNoSource;
     if (r.e < 0) return s;
     ExpertRows rows = expert_rows(g.offsets, g.counts, r.e, g.rows);
+    if constexpr (PARTS) {
+      const int each = ((rows.count + parts - 1) / parts + kStepRows - 1) / kStepRows * kStepRows;
+      const int first = min(r.part * each, rows.count);
+      rows.start += first;
+      rows.count = min(rows.count - first, each);
+    }
     // the same in every lane: into scalar registers, where buffer resources live
     rows.start = __builtin_amdgcn_readfirstlane(rows.start);
     rows.count = __builtin_amdgcn_readfirstlane(rows.count);
@@ -258,12 +277,29 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
     const Source following = source(next);
     f32x4 acc[S::FI][S::FJ];
     multiply<S, S::FI>(lds, feed, cur, following, at, [](int) { return 0; }, acc);
-    at.younger = store_tile<S, S::FI>(lds, acc, g.out + (static_cast<int64_t>(t.e) * g.n + t.i0) * g.k + t.j0,
-                                      g.k, g.n - t.i0, g.k - t.j0);
+    const int64_t row = static_cast<int64_t>(PARTS ? t.part * g.n_experts + t.e : t.e) * g.n + t.i0;
+    if constexpr (PARTS)
+      at.younger = store_tile<S, S::FI>(lds, acc, g.parts + row * g.k + t.j0, g.k, g.n - t.i0, g.k - t.j0);
+    else
+      at.younger = store_tile<S, S::FI>(lds, acc, g.out + row * g.k + t.j0, g.k, g.n - t.i0, g.k - t.j0);
     t = next;
     cur = following;
   }
   wait_and_meet<0>();  // loads past the last tile fetch nothing, but write LDS
+}
+
+// dw from its parts, in their order: 8 values a thread.
+__global__ __launch_bounds__(256) void join_kernel(ProductArgs g, int parts, int64_t vectors) {
+  for (int64_t v = blockIdx.x * 256ll + threadIdx.x; v < vectors; v += gridDim.x * 256ll) {
+    f32x4 lo{0.f, 0.f, 0.f, 0.f}, hi = lo;
+    for (int q = 0; q < parts; ++q) {
+      const f32x4 *from = reinterpret_cast<const f32x4 *>(g.parts + (q * vectors + v) * 8);
+      lo += from[0];
+      hi += from[1];
+    }
+    const float sum[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+    store8(g.out + v * 8, sum);
+  }
 }
 
 template <class S>
@@ -280,8 +316,23 @@ hipError_t launch_dw(ProductArgs g, hipStream_t stream) {
   g.col_tiles = (g.k + S::BJ - 1) / S::BJ;
   const int row_tiles = (g.n + S::BI - 1) / S::BI;
   const int64_t total = static_cast<int64_t>(g.n_experts) * row_tiles * g.col_tiles;
-  dw_kernel<S><<<tile_grid(total, S::kResident), S::kThreads, 0, stream>>>(g, row_tiles,
-                                                                          static_cast<int>(total));
+  dw_kernel<S, false><<<tile_grid(total, S::kResident), S::kThreads, 0, stream>>>(g, row_tiles,
+                                                                                 static_cast<int>(total), 1);
+  return hipGetLastError();
+}
+
+template <class S>
+hipError_t launch_dw_parts(ProductArgs g, int parts, hipStream_t stream) {
+  g.col_tiles = (g.k + S::BJ - 1) / S::BJ;
+  const int row_tiles = (g.n + S::BI - 1) / S::BI;
+  const int64_t total = static_cast<int64_t>(g.n_experts) * row_tiles * g.col_tiles * parts;
+  dw_kernel<S, true><<<tile_grid(total, S::kResident), S::kThreads, 0, stream>>>(g, row_tiles,
+                                                                                static_cast<int>(total), parts);
+  const hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return err;
+  const int64_t vectors = static_cast<int64_t>(g.n_experts) * g.n * g.k / 8, blocks = (vectors + 255) / 256;
+  join_kernel<<<static_cast<uint32_t>(blocks < 4 * kComputeUnits ? blocks : 4 * kComputeUnits), 256, 0, stream>>>(
+      g, parts, vectors);
   return hipGetLastError();
 }
 
@@ -299,10 +350,11 @@ hipError_t launch_dx_sized(const ProductArgs &g, int64_t pairs, hipStream_t stre
 // (2N = K = 1024: 8 experts, 128 tiles of 256 x 256, 31.6 us, of 128 x 128, 22.3;
 // 16 experts, 256 tiles, 12.8 and 13.3; 2 experts with 2N = 512, K = 256 and 8192 rows,
 // 16 tiles of 128 x 128, 79.7, of 64 x 64, 49.5.)
-hipError_t launch_dw_sized(const ProductArgs &g, hipStream_t stream) {
+hipError_t launch_dw_sized(const ProductArgs &g, int parts, hipStream_t stream) {
   typedef Shape<256, 256, 2, 4, 2, true, true> Large;
   typedef Shape<128, 128, 2, 2, 2, true, true> Middle;
   typedef Shape<64, 64, 2, 2, 6, true, true> Small;
+  if (parts > 1) return launch_dw_parts<Shape<kDwTile, kDwTile, 2, 2, 6, true, true>>(g, parts, stream);
   auto tiles = [&](auto shape) {
     typedef decltype(shape) S;
     return g.n_experts * col_tiles<S::BI>(g.n) * col_tiles<S::BJ>(g.k);
@@ -350,6 +402,7 @@ hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, co
   a.rows = static_cast<int>(max_rows(p));
   a.k = op.in_dim;
   a.n = width;
+  a.parts = nullptr;
   if (b.dx) {
     a.out = b.dx;
     err = launch_dx_sized(a, pairs, stream);
@@ -357,7 +410,8 @@ hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, co
   }
   if (b.dw) {
     a.out = b.dw;
-    err = launch_dw_sized(a, stream);
+    a.parts = reinterpret_cast<float *>(static_cast<char *>(b.workspace) + expert_bias_bytes(p, op));
+    err = launch_dw_sized(a, dw_parts(p, width, op.in_dim), stream);
   }
   return err;
 }

@@ -64,11 +64,6 @@ struct Shape {
   static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_;
   static constexpr bool XI = XI_, XJ = XJ_, FP8 = FP8_;
   static constexpr int kThreads = WI * WJ * kWave;
-  // at least two waves a SIMD: that also keeps the accumulators in the 256
-  // registers that both operands and results of an MFMA can name (with more, the
-  // compiler moves them to and from the accumulation registers in the loop)
-  // (a workgroup of one wave is held to fewer by its LDS)
-  static constexpr int kWavesPerSimd = WI * WJ >= 4 ? 2 : 1;
   static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
   // 16-byte loads a thread makes for an operand in a step; a tile smaller than one load
   // of every thread still gets a whole one (its spare rows are zeros)
@@ -85,6 +80,11 @@ struct Shape {
   // workgroups that a compute unit holds: LDS, and two waves a SIMD
   static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (WI * WJ);
   static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
+  // Two waves a SIMD also keep the accumulators in the 256 registers that both
+  // operands and results of an MFMA can name (with more, the compiler moves them to
+  // and from the accumulation registers in the loop).  Small tiles with many
+  // stages are held to one by their LDS.
+  static constexpr int kWavesPerSimd = kResident * WI * WJ >= 8 ? 2 : 1;
   static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // of a wave and stage
   static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
   static_assert(kLoads * (NST - 1) < 64, "the wait counter holds 63 loads");
@@ -567,6 +567,13 @@ __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, c
   __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0, 0);
 }
 
+__device__ __forceinline__ void store8_f32(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {
+  typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+  const f32x4 lo{v[0], v[1], v[2], v[3]}, hi{v[4], v[5], v[6], v[7]};
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, lo), r, static_cast<int>(off), 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, hi), r, static_cast<int>(off), 16, 0);
+}
+
 // ---------------------------------------------------------- expert rows ---
 
 // Rows of expert e that hold a token, whatever the plan's arrays hold:
@@ -617,8 +624,11 @@ struct RowTiles {
     mine = 0;
     for (int u = 0; u < per; ++u) {
       const int e = lane_id() * per + u;
-      if (e < n_experts) mine += (expert_rows(offsets, counts, e, rows).count + BI - 1) / BI;
+      if (e < n_experts) mine += min((expert_rows(offsets, counts, e, rows).count + BI - 1) / BI, 1 << 24);
     }
+    // (2^24 row tiles are more than any routing within check_expert_op's limits has; plan
+    // arrays that describe none cannot make the sums below overflow)
+    mine = min(mine, 1 << 24);
     incl = wave_incl_scan(mine);
     total = static_cast<int64_t>(__builtin_amdgcn_readlane(incl, kWave - 1)) * col_tiles;
     chunk = (total + 7) / 8;

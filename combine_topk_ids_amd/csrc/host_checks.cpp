@@ -112,9 +112,30 @@ int64_t expert_capacity(int64_t n_tokens, int32_t top_k, int32_t n_experts, doub
   return static_cast<int64_t>(cap);
 }
 
-size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op) {
+int dw_parts(const moe_problem &p, int64_t n, int64_t k) {
+  const int64_t tiles = p.n_experts * ((n + kDwTile - 1) / kDwTile) * ((k + kDwTile - 1) / kDwTile);
+  const int64_t pairs = expert_row_bound(p), used = pairs < p.n_experts ? pairs : p.n_experts;
+  if (used == 0 || tiles > kDwWorkgroups / 2) return 1;
+  int64_t parts = kDwWorkgroups / tiles;
+  if (parts > pairs / used / kDwPartRows) parts = pairs / used / kDwPartRows;
+  if (parts > kDwMostParts) parts = kDwMostParts;
+  return parts > 1 ? static_cast<int>(parts) : 1;
+}
+
+size_t expert_bias_bytes(const moe_problem &p, const moe_expert_op &op) {
   const size_t chunks = static_cast<size_t>(max_rows(p)) / kBiasChunkRows + p.n_experts + 1;
   return align256(chunks * 2 * static_cast<size_t>(op.out_dim) * sizeof(float));
+}
+
+size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op) {
+  size_t most = 0;
+  for (int wide = 1; wide <= 2; ++wide) {  // the linear layer's weights, and the gated block's
+    const int64_t n = wide * static_cast<int64_t>(op.out_dim);
+    const int parts = dw_parts(p, n, op.in_dim);
+    const size_t b = parts > 1 ? static_cast<size_t>(parts) * p.n_experts * n * op.in_dim * sizeof(float) : 0;
+    if (b > most) most = b;
+  }
+  return expert_bias_bytes(p, op) + align256(most);
 }
 
 namespace host {
@@ -423,7 +444,7 @@ int check_expert_backward_args(const moe_problem *p, const moe_plan *plan, const
   const bool rows = expert_row_bound(*p) > 0;
   if (rows && (!dy || (through_act && (!preact || !dz)))) return MOE_EINVAL;
   if (rows && ((dx && !w) || (dw && !x))) return MOE_EINVAL;
-  if (dbias && !workspace) return MOE_EINVAL;
+  if ((dw || dbias) && !workspace) return MOE_EINVAL;
   if (!aligned(dy, 16) || !aligned(preact, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dz, 16) ||
       !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(workspace, 256) ||
       !aligned(plan->expert_counts, 4) || !aligned(plan->expert_offsets, 4))

@@ -90,10 +90,17 @@ inline int64_t expert_row_bound(const moe_problem &p) {
   return pairs < rows ? pairs : rows;
 }
 
+// Parts that the rows of an expert are split into for its weights' gradient
+// [E][n][k]: more than one where 64 x 64 tiles of it would leave most compute units
+// without work and the rows are many.  At most kDwWorkgroups workgroups.
+constexpr int kDwTile = 64, kDwWorkgroups = 512, kDwMostParts = 16, kDwPartRows = 256;
+int dw_parts(const moe_problem &p, int64_t n, int64_t k);
+
 // Workspace of the experts' backward passes: column sums of dz over 64-row
 // chunks of each expert (at most rows / 64 + E of them, up to 2 * out_dim
-// columns), for dbias.
+// columns), for dbias; then the parts of dw, fp32.
 constexpr int kBiasChunkRows = 64;
+size_t expert_bias_bytes(const moe_problem &p, const moe_expert_op &op);
 size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op);
 
 // ---- argument checks: MOE_OK or the code the entry point returns -----------

@@ -432,6 +432,14 @@ def moe_combine(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor,
     _checked(rc, "moe_combine")
 
 
+def _on_current_device(plan: PlanBuffers, *tensors) -> None:
+    """The kernels run on the current device's stream: every buffer must live there."""
+    here = torch.cuda.current_device()
+    for t in (plan.slot, plan.expert_counts, plan.expert_offsets, *tensors):
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+
+
 def moe_combine_backward(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor | None,
                          topk_weights: torch.Tensor | None, dout: torch.Tensor, dy: torch.Tensor,
                          dweights: torch.Tensor | None = None, stream=None) -> None:
@@ -444,6 +452,8 @@ def moe_combine_backward(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor
     d = _dev(dout, "dout", _BF16, p.n_tokens * p.hidden)
     o = _dev(dy, "dy", _BF16, r_max * p.hidden)
     dw = _dev(dweights, "dweights", (torch.float32,), npairs) or None
+    _dev(plan.slot, "plan.slot", (torch.int32,), npairs)
+    _on_current_device(plan, expert_out, topk_weights, dout, dy, dweights)
     rc = lib.moe_combine_backward(ctypes.byref(p), ctypes.byref(plan.as_struct()), y, w, d, o, dw,
                                   _stream(stream))
     _checked(rc, "moe_combine_backward")
@@ -466,11 +476,16 @@ def moe_expert_workspace_bytes(p: Problem, op: ExpertOp) -> int:
 
 
 def alloc_expert_workspace(p: Problem, op: ExpertOp, device="cuda") -> torch.Tensor:
-    """Scratch of the backward calls with a dbias."""
+    """Scratch of the backward calls with a dw or a dbias."""
     nbytes = moe_expert_workspace_bytes(p, op)
     if nbytes == 0:
         raise MoeError(moe_check_expert_op(p, op), "alloc_expert_workspace")
     return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+def _plan_rows(plan: PlanBuffers, experts: int) -> None:
+    _dev(plan.expert_counts, "plan.expert_counts", (torch.int32,), experts)
+    _dev(plan.expert_offsets, "plan.expert_offsets", (torch.int32,), experts + 1)
 
 
 def _expert_forward(name, fn, wide, p, plan, op, x, w, y, x_scales, w_scales, bias, preact,
@@ -485,6 +500,8 @@ def _expert_forward(name, fn, wide, p, plan, op, x, w, y, x_scales, w_scales, bi
             _dev(bias, "bias", (torch.float32,), e * wide * n) or None]
     args += [_dev(r, "residual", _BF16, rows * n) or None for r in residual]
     args += [_dev(y, "y", _BF16, rows * n), _dev(preact, "preact", _BF16, rows * wide * n) or None]
+    _plan_rows(plan, e)
+    _on_current_device(plan, x, x_scales, w, w_scales, bias, *residual, y, preact)
     return fn, name, (ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args)
 
 
@@ -514,7 +531,7 @@ def moe_expert_linear(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tens
 def _expert_backward(name, fn, wide, p, plan, op, dy, preact, x, w, dz, dx, dw, dbias, workspace,
                      stream):
     rows, e, k, n = _sizes(p)[0], p.n_experts, op.in_dim, op.out_dim
-    ws = moe_expert_workspace_bytes(p, op) if dbias is not None else None
+    ws = moe_expert_workspace_bytes(p, op) if dw is not None or dbias is not None else None
     args = (_dev(dy, "dy", _BF16, rows * n),
             _dev(preact, "preact", _BF16, rows * wide * n) or None,
             _dev(x, "x", _BF16, rows * k) or None,
@@ -524,6 +541,8 @@ def _expert_backward(name, fn, wide, p, plan, op, dy, preact, x, w, dz, dx, dw, 
             _dev(dw, "dw", _BF16, e * wide * n * k) or None,
             _dev(dbias, "dbias", (torch.float32,), e * wide * n) or None,
             _dev(workspace, "workspace", (torch.uint8,), ws) or None)
+    _plan_rows(plan, e)
+    _on_current_device(plan, dy, preact, x, w, dz, dx, dw, dbias, workspace)
     rc = fn(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args, _stream(stream))
     _checked(rc, name)
 
@@ -534,7 +553,7 @@ def moe_expert_glu_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dh: tor
                             dbias: torch.Tensor | None = None,
                             workspace: torch.Tensor | None = None, stream=None) -> None:
     """Gradients of moe_expert_glu; dx, dw and dbias may be None (not
-    computed).  dbias needs a workspace (alloc_expert_workspace)."""
+    computed).  dw and dbias need a workspace (alloc_expert_workspace)."""
     _expert_backward("moe_expert_glu_backward", lib.moe_expert_glu_backward, 2, p, plan, op, dh,
                      preact, x, w, dz, dx, dw, dbias, workspace, stream)
 
@@ -545,7 +564,8 @@ def moe_expert_linear_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dy: 
                                preact: torch.Tensor | None = None, dz: torch.Tensor | None = None,
                                dbias: torch.Tensor | None = None,
                                workspace: torch.Tensor | None = None, stream=None) -> None:
-    """Gradients of moe_expert_linear; preact and dz with an activation only."""
+    """Gradients of moe_expert_linear; preact and dz with an activation only.
+    dw and dbias need a workspace (alloc_expert_workspace)."""
     _expert_backward("moe_expert_linear_backward", lib.moe_expert_linear_backward, 1, p, plan, op, dy,
                      preact, x, w, dz, dx, dw, dbias, workspace, stream)
 

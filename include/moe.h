@@ -397,8 +397,8 @@ typedef struct moe_expert_op { /* host memory */
 /* MOE_OK if op is well formed for p, else the code the calls below return. */
 MOE_API int moe_check_expert_op(const moe_problem *p, const moe_expert_op *op);
 
-/* Device scratch bytes of the backward calls with a dbias (0 for an invalid
- * op).  256-byte aligned, caller-owned, needs no initialisation; two calls
+/* Device scratch bytes of the backward calls with a dw or a dbias (0 for an
+ * invalid op).  256-byte aligned, caller-owned, needs no initialisation; two calls
  * that may overlap (two streams, two captured graphs) need one each. */
 MOE_API size_t moe_expert_workspace_bytes(const moe_problem *p, const moe_expert_op *op);
 
@@ -434,8 +434,9 @@ MOE_API int moe_expert_linear(const moe_problem *p, const moe_plan *plan, const 
  * dz is an output and required: it is rounded to bf16 there, and dx and dw are
  * products of the rounded values; dbias sums the unrounded ones.  dx, dw and
  * dbias may each be NULL (not computed).  dw and dbias are written whole, zeros
- * for experts without rows.  workspace: moe_expert_workspace_bytes, needed
- * with dbias only. */
+ * for experts without rows.  (Where few weights meet many rows, the rows' parts
+ * of dw are summed in fp32, in order, before the rounding.)  workspace:
+ * moe_expert_workspace_bytes, needed with dw or dbias. */
 MOE_API int moe_expert_glu_backward(const moe_problem *p, const moe_plan *plan,
                                     const moe_expert_op *op, const uint16_t *dh,
                                     const uint16_t *preact, const uint16_t *x,

@@ -76,6 +76,12 @@ SIZES = [
     dict(tokens=90, experts=1024, top_k=4, k=64, f=40),
     dict(tokens=33, experts=4, top_k=2, k=256, f=256, masked=1.0),
     dict(tokens=2500, experts=3, top_k=1, k=264, f=520, skew=2.0, bias=True),
+    # few weights and many rows: dw in parts
+    dict(tokens=6000, experts=2, top_k=1, k=136, f=72, skew=1.0, bias=True),
+    # past the small tiles: enough tiles of 128 x 128, and of 256 x 256, in every product
+    dict(tokens=2500, experts=3, top_k=1, k=776, f=1032, bias=True),
+    dict(tokens=2000, experts=8, top_k=2, k=1400, f=1552, masked=0.05, skew=0.3, act="gelu_tanh", bias=True),
+    dict(tokens=1100, experts=64, top_k=6, k=1032, f=264, pad=16),
 ]
 
 
@@ -130,6 +136,9 @@ FP8_SIZES = [
     dict(tokens=150, experts=4, top_k=2, k=512, f=384, act="gelu_tanh", masked=0.2),
     dict(tokens=700, experts=2, top_k=1, k=256, f=128, pad=128, bias=True),
     dict(tokens=64, experts=128, top_k=8, k=256, f=128, act="relu"),
+    # enough tiles: workgroups that take tile after tile, and one workgroup a tile
+    dict(tokens=300, experts=64, top_k=6, k=384, f=256, pad=16, bias=True),
+    dict(tokens=3000, experts=4, top_k=1, k=512, f=768, skew=0.5, bias=True),
 ]
 
 
