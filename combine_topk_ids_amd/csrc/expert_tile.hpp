@@ -560,11 +560,12 @@ __device__ __forceinline__ bf16x8 round8(const float (&v)[8]) {
 __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
   *reinterpret_cast<bf16x8 *>(p) = round8(v);
 }
-// Through a buffer resource, at byte `off`; kNowhere drops it.  Always one store of
+// Through a buffer resource, at byte `off`; kNowhere drops it.  POLICY: cache bits.  Always one store of
 // the wave, whichever lanes have something to store (wait_behind counts them).
+template <int POLICY = kLoadDefault>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0, 0);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0, POLICY);
 }
 
 __device__ __forceinline__ void store8_f32(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {

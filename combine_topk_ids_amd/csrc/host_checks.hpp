@@ -96,10 +96,10 @@ inline int64_t expert_row_bound(const moe_problem &p) {
 constexpr int kDwTile = 64, kDwWorkgroups = 512, kDwMostParts = 16, kDwPartRows = 256;
 int dw_parts(const moe_problem &p, int64_t n, int64_t k);
 
-// Workspace of the experts' backward passes: column sums of dz over 64-row
-// chunks of each expert (at most rows / 64 + E of them, up to 2 * out_dim
+// Workspace of the experts' backward passes: column sums of dz over 16-row
+// chunks of each expert (at most rows / 16 + E of them, up to 2 * out_dim
 // columns), for dbias; then the parts of dw, fp32.
-constexpr int kBiasChunkRows = 64;
+constexpr int kBiasChunkRows = 16;
 size_t expert_bias_bytes(const moe_problem &p, const moe_expert_op &op);
 size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op);
 

@@ -65,15 +65,15 @@ def test_an_invalid_problem_is_refused_first(moe):
 
 
 def test_workspace_holds_the_column_sums(moe):
-    """One row of 2 * out_dim fp32 sums for every 64-row chunk of every expert: an
-    expert's n rows touch at most n / 64 + 1 chunks."""
+    """One row of 2 * out_dim fp32 sums for every 16-row chunk of every expert: an
+    expert's n rows touch at most n / 16 + 1 chunks."""
     p, op = moe.problem(1000, 256, 3, 8, 4, pad_multiple=16), moe.expert_op(256, 72)
-    need = (moe.moe_max_rows(p) // 64 + 8) * 2 * 72 * 4
+    need = (moe.moe_max_rows(p) // 16 + 8) * 2 * 72 * 4
     got = moe.moe_expert_workspace_bytes(p, op)
     assert need <= got <= need + 4096 and got % 256 == 0
     # few weights and many rows: dw's parts too, 2 experts x 144 x 136 of fp32, 16 of them
     p, op = moe.problem(20000, 64, 1, 2, 1), moe.expert_op(136, 72)
-    need = (moe.moe_max_rows(p) // 64 + 2) * 2 * 72 * 4 + 16 * 2 * 144 * 136 * 4
+    need = (moe.moe_max_rows(p) // 16 + 2) * 2 * 72 * 4 + 16 * 2 * 144 * 136 * 4
     assert need <= moe.moe_expert_workspace_bytes(p, op) <= need + 4096
 
 
