@@ -432,12 +432,19 @@ def moe_combine(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor,
     _checked(rc, "moe_combine")
 
 
-def _on_current_device(plan: PlanBuffers, *tensors) -> None:
-    """The kernels run on the current device's stream: every buffer must live there."""
-    here = torch.cuda.current_device()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _own_stream(stream, plan: PlanBuffers, *tensors) -> int:
+    """The raw stream to launch on; the kernels run on the current device, so every
+    buffer must live there."""
+    here = _current_device()
     for t in (plan.slot, plan.expert_counts, plan.expert_offsets, *tensors):
         if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(here) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
 
 
 def moe_combine_backward(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor | None,
@@ -453,9 +460,8 @@ def moe_combine_backward(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor
     o = _dev(dy, "dy", _BF16, r_max * p.hidden)
     dw = _dev(dweights, "dweights", (torch.float32,), npairs) or None
     _dev(plan.slot, "plan.slot", (torch.int32,), npairs)
-    _on_current_device(plan, expert_out, topk_weights, dout, dy, dweights)
     rc = lib.moe_combine_backward(ctypes.byref(p), ctypes.byref(plan.as_struct()), y, w, d, o, dw,
-                                  _stream(stream))
+                                  _own_stream(stream, plan, expert_out, topk_weights, dout, dy, dweights))
     _checked(rc, "moe_combine_backward")
 
 
@@ -489,7 +495,7 @@ def _plan_rows(plan: PlanBuffers, experts: int) -> None:
 
 
 def _expert_forward(name, fn, wide, p, plan, op, x, w, y, x_scales, w_scales, bias, preact,
-                    residual=()):
+                    stream, residual=()):
     rows, e, k, n = _sizes(p)[0], p.n_experts, op.in_dim, op.out_dim
     fp8 = op.fmt == FMT["fp8"]
     codes = (torch.uint8, torch.float8_e4m3fn) if fp8 else _BF16
@@ -501,8 +507,8 @@ def _expert_forward(name, fn, wide, p, plan, op, x, w, y, x_scales, w_scales, bi
     args += [_dev(r, "residual", _BF16, rows * n) or None for r in residual]
     args += [_dev(y, "y", _BF16, rows * n), _dev(preact, "preact", _BF16, rows * wide * n) or None]
     _plan_rows(plan, e)
-    _on_current_device(plan, x, x_scales, w, w_scales, bias, *residual, y, preact)
-    return fn, name, (ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args)
+    raw = _own_stream(stream, plan, x, x_scales, w, w_scales, bias, *residual, y, preact)
+    _checked(fn(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args, raw), name)
 
 
 def moe_expert_glu(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor, w: torch.Tensor,
@@ -511,9 +517,8 @@ def moe_expert_glu(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor,
                    preact: torch.Tensor | None = None, stream=None) -> None:
     """Gated block over the packed rows: h = act(z[:, :F]) * z[:, F:] with
     z = x w_e^T + bias_e; w [E, 2F, K], gate rows first."""
-    fn, name, args = _expert_forward("moe_expert_glu", lib.moe_expert_glu, 2, p, plan, op, x, w, h,
-                                     x_scales, w_scales, bias, preact)
-    _checked(fn(*args, _stream(stream)), name)
+    _expert_forward("moe_expert_glu", lib.moe_expert_glu, 2, p, plan, op, x, w, h, x_scales, w_scales,
+                    bias, preact, stream)
 
 
 def moe_expert_linear(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor, w: torch.Tensor,
@@ -523,9 +528,8 @@ def moe_expert_linear(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tens
                       stream=None) -> None:
     """Linear layer over the packed rows: y = act(x w_e^T + bias_e) + residual;
     w [E, F, K]."""
-    fn, name, args = _expert_forward("moe_expert_linear", lib.moe_expert_linear, 1, p, plan, op, x, w,
-                                     y, x_scales, w_scales, bias, preact, (residual,))
-    _checked(fn(*args, _stream(stream)), name)
+    _expert_forward("moe_expert_linear", lib.moe_expert_linear, 1, p, plan, op, x, w, y, x_scales,
+                    w_scales, bias, preact, stream, (residual,))
 
 
 def _expert_backward(name, fn, wide, p, plan, op, dy, preact, x, w, dz, dx, dw, dbias, workspace,
@@ -542,9 +546,8 @@ def _expert_backward(name, fn, wide, p, plan, op, dy, preact, x, w, dz, dx, dw, 
             _dev(dbias, "dbias", (torch.float32,), e * wide * n) or None,
             _dev(workspace, "workspace", (torch.uint8,), ws) or None)
     _plan_rows(plan, e)
-    _on_current_device(plan, dy, preact, x, w, dz, dx, dw, dbias, workspace)
-    rc = fn(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args, _stream(stream))
-    _checked(rc, name)
+    raw = _own_stream(stream, plan, dy, preact, x, w, dz, dx, dw, dbias, workspace)
+    _checked(fn(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args, raw), name)
 
 
 def moe_expert_glu_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dh: torch.Tensor,
