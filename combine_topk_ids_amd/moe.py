@@ -1,4 +1,4 @@
-"""ctypes binding of libmoe (HIP, gfx950): MoE dispatch plan, dispatch, combine.
+"""ctypes binding of libmoe (HIP, gfx950): MoE dispatch plan, dispatch, experts, combine.
 
 Argument marshalling only: every step of the path runs in libmoe's kernels.
 PyTorch supplies device memory (tensors' ``data_ptr()``) and the stream

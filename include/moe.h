@@ -5,7 +5,8 @@
  * The library turns top-k expert IDs into a routing plan, packs token rows
  * into an expert-major buffer (optionally quantised to blockwise FP8,
  * MX-FP4 or NVFP4 on the way) and combines expert outputs back into token
- * order, weighted by the gate values.  Expert-parallel destination ranks
+ * order, weighted by the gate values.  It also runs the experts' products on
+ * the packed rows, and the backward passes of products and combine.  Expert-parallel destination ranks
  * are simulated as contiguous segments of the one packed buffer, or, with
  * the moe_exchange_* calls, as separate receive buffers of several
  * simulated source ranks.
