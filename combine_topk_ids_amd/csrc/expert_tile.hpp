@@ -9,7 +9,7 @@
 // the weights in the rows' gradient, both operands of the weights' gradient).
 //
 // J is the MFMA's A operand and I its B operand, so that a lane ends with four
-// neighbouring j of one i: 8-byte stores of bf16, and one row scale per lane.
+// neighbouring j of one i, under one row scale.
 //
 // Memory path.  A step covers 128 bytes of the contraction (64 bf16 or 128 E4M3
 // values).  Tiles go from global memory straight into LDS (16 bytes a lane, no
@@ -26,7 +26,7 @@
 //   across c: rows of 16-column groups (32 bytes), group g of row r at
 //             g ^ f(r), f taking r's bits 0, 1, 3, 4: the 16 rows that one
 //             transposing read visits for one group then lie in different banks.
-// (Counters: no bank conflict in any of the products.)
+// (Counters: no bank conflict in the bf16 products.)
 // Where an operand ends, the buffer resource ends: loads past it fetch nothing and
 // leave zeros in LDS.  What a lane adds to the resource's base is the same for
 // every tile; a tile is a few scalars.
@@ -42,7 +42,6 @@ namespace tile {
 
 #define MOE_LDS __attribute__((address_space(3)))
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
@@ -112,7 +111,8 @@ __device__ __forceinline__ i32x4 resource(const void *base, uint32_t bytes) {
 // its prefetch to that).  These loads have no register results; what waits for them
 // is wait_and_meet.  First line: scalars written by a vector instruction just before
 // need five cycles; after a write of m0, one.
-#define MOE_TO_LDS(N) "s_add_u32 m0, m0, %[stride]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o" #N "], %[r], 0 offen lds\n\t"
+#define MOE_TO_LDS(N) \
+  "s_add_u32 m0, m0, %[stride]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o" #N "], %[r], 0 offen lds\n\t"
 #define MOE_TO_LDS_FIRST \
   "s_nop 4\n\ts_mov_b32 m0, %[to]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o0], %[r], 0 offen lds\n\t"
 template <int STRIDE, int L>
@@ -418,8 +418,7 @@ __device__ __forceinline__ void multiply(lds_ptr lds, const F &feed, const Sourc
   if constexpr (S::FP8) {
     // A phase for each block of I: its products run while the next block's rows are
     // read.  In a step's last phase each block of J makes way, after its product,
-    // for the next step's.  (Reading further ahead would not leave registers for
-    // 128 sums.)
+    // for the next step's.
     i32x8 vi[2], vj[S::FJ];
     float si[2], sj[S::FJ];
     auto read_i = [&](int set, int blk) {
@@ -548,9 +547,6 @@ struct Transpose {
   }
 };
 
-__device__ __forceinline__ void load8(const uint16_t *p, float (&v)[8]) {
-  unpack8(*reinterpret_cast<const uint4 *>(p), v);
-}
 __device__ __forceinline__ bf16x8 round8(const float (&v)[8]) {
   bf16x8 r;
 #pragma unroll
@@ -560,12 +556,14 @@ __device__ __forceinline__ bf16x8 round8(const float (&v)[8]) {
 __device__ __forceinline__ void store8(uint16_t *p, const float (&v)[8]) {
   *reinterpret_cast<bf16x8 *>(p) = round8(v);
 }
-// Through a buffer resource, at byte `off`; kNowhere drops it.  POLICY: cache bits.  Always one store of
-// the wave, whichever lanes have something to store (wait_behind counts them).
+// Through a buffer resource, at byte `off`; kNowhere drops it.  POLICY: cache bits.
+// Always one store of the wave, whichever lanes have something to store
+// (wait_behind counts them).
 template <int POLICY = kLoadDefault>
 __device__ __forceinline__ void store8(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {
   typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
-  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0, POLICY);
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, round8(v)), r, static_cast<int>(off), 0,
+                                         POLICY);
 }
 
 __device__ __forceinline__ void store8_f32(__amdgpu_buffer_rsrc_t r, uint32_t off, const float (&v)[8]) {
@@ -646,7 +644,9 @@ struct RowTiles {
     const int64_t t = (blockIdx.x % 8) * chunk + pos;
     // (past the end in one round is past it in every later one)
     if (pos >= chunk || t >= total) return r;
-    const int owner = __builtin_ctzll(ballot(static_cast<int64_t>(incl) * col_tiles > t));
+    const uint64_t past = ballot(static_cast<int64_t>(incl) * col_tiles > t);
+    if (past == 0) return r;
+    const int owner = __builtin_ctzll(past);
     int before = __builtin_amdgcn_readlane(incl - mine, owner);
     // the owner's experts, one per lane
     const int lane = lane_id(), e = owner * per + lane;
@@ -654,7 +654,9 @@ struct RowTiles {
     if (lane < per && e < n_experts) x = expert_rows(offsets, counts, e, rows);
     const int tiles = (x.count + BI - 1) / BI;
     const int upto = wave_incl_scan(tiles);
-    const int who = __builtin_ctzll(ballot(static_cast<int64_t>(before + upto) * col_tiles > t));
+    const uint64_t here = ballot(static_cast<int64_t>(before + upto) * col_tiles > t);
+    if (here == 0) return r;  // the plan changed since init()
+    const int who = __builtin_ctzll(here);
     r.e = owner * per + who;
     r.start = __builtin_amdgcn_readlane(x.start, who);
     r.count = __builtin_amdgcn_readlane(x.count, who);

@@ -370,7 +370,9 @@ MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
  * Sums are fp32 (MFMA accumulators); results are rounded to bf16 once, when they
  * are stored.  Each result depends on its own row, weights and bias alone, and
  * runs repeat bit for bit.  An infinity or NaN in a row or in an expert's weights
- * reaches the results of that row or expert only.
+ * reaches the results of that row or expert only.  Outputs must not overlap
+ * inputs or each other (but the residual may be y itself); the plan must not
+ * change while a call runs.
  *
  * p names the packed buffer (R_max rows, E experts); its hidden and fmt are not
  * used here.  Needs in_dim, out_dim <= 2^20, in_dim * out_dim < 2^29 and

@@ -384,3 +384,43 @@ def test_parts_of_the_gradients(moe):
         got = run((part,))
         assert torch.equal(bits(got["dz"]), bits(whole["dz"]))
         assert torch.equal(bits(got[part]), bits(whole[part]))
+
+
+def test_offsets_past_32_bits(moe):
+    """Rows, results and weights of more than 4 GiB: the last expert's last rows."""
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GiB of device memory")
+    tokens, experts, k, f = 150_000, 3, 16_384, 24
+    r = Routed(moe, 50, tokens, experts, 1, hidden=8)
+    a, b = r.ranges[-1]
+    assert b == tokens and b * k * 2 > 1 << 32
+    tail = slice(b - 40, b)
+    x = torch.empty(r.rows, k, dtype=torch.bfloat16, device="cuda").normal_(generator=r.g)
+    w = weights(r, f, k)
+    y = r.sentinel(f)
+    moe.moe_expert_linear(r.p, r.plan, moe.expert_op(k, f), x, w, y)
+    torch.cuda.synchronize()
+    _, ry, _, ty = ref.forward(x[tail].double(), w[-1].double(), None, False, "none")
+    assert_within(y[tail], ry, ty, "y of rows past 4 GiB")
+    # and as results: dx of the same size, with dw over all of the expert's rows
+    d, dw = r.randn(r.rows, f).bfloat16(), torch.empty_like(w)
+    dx = torch.full((r.rows, k), -77.0, dtype=torch.bfloat16, device="cuda")
+    op = moe.expert_op(k, f)
+    moe.moe_expert_linear_backward(r.p, r.plan, op, d, x, w, dx, dw, workspace=moe.alloc_expert_workspace(r.p, op))
+    torch.cuda.synchronize()
+    dt = d[tail].double()
+    assert_within(dx[tail], dt @ w[-1].double(), ref.product_bound(dt, w[-1].double(), f), "dx past 4 GiB")
+    dc, xc = d[a:b, :8].double(), x[a:b, -64:].double()
+    assert_within(dw[-1, :8, -64:], dc.T @ xc, ref.product_bound(dc.T, xc, b - a), "dw over rows past 4 GiB")
+    del x, dx, dw
+    # weights: 70 experts of 64 MiB, the last one's result
+    r = Routed(moe, 51, 20, 70, 2, only=(0, 69), hidden=8)
+    k, f = 4096, 8192
+    w = torch.empty(70, f, k, dtype=torch.bfloat16, device="cuda").normal_(0, k ** -0.5, generator=r.g)
+    x, y = r.packed(k), r.sentinel(f)
+    moe.moe_expert_linear(r.p, r.plan, moe.expert_op(k, f), x, w, y)
+    torch.cuda.synchronize()
+    for e in (0, 69):
+        a, b = r.ranges[e]
+        _, ry, _, ty = ref.forward(x[a:b].double(), w[e].double(), None, False, "none")
+        assert_within(y[a:b], ry, ty, f"y of expert {e}")
