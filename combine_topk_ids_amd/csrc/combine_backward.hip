@@ -9,10 +9,10 @@
 // rows of at most 512 columns, one wave); the waves take the token's 512-column
 // chunks in turn (8 columns a lane) and keep the k dot products in registers; at the
 // end the lanes' sums are added in a fixed order, so runs repeat bit for bit.
-// Measured: 8192 tokens, k = 8, H = 7168: 400 us, 4.9 TB/s, what a copy reaches.  A masked slot (or one
-// outside the rows) gets a buffer resource of zero bytes: its loads return
-// zeros and its stores are dropped by the hardware, with no branch between the
-// chunk's loads.  A token's rows are its own (slots are distinct), so no
+// Measured: 8192 tokens, k = 8, H = 7168: 400 us, 4.9 TB/s, what a copy reaches.  A
+// masked slot (or one outside the rows) gets a buffer resource of zero bytes: its
+// loads return zeros and its stores are dropped by the hardware, with no branch
+// between the chunk's loads.  A token's rows are its own (slots are distinct), so no
 // two workgroups write one row.
 #include "moe_device.hpp"
 #include "moe_kernels.hpp"

@@ -34,9 +34,9 @@ struct GateUpRow {
 };
 
 template <class S, bool GLU, int ACT>
-__global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void forward_kernel(ForwardArgs g) {
+__global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void forward_kernel(ForwardArgs g) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
-  lds_ptr lds = (lds_ptr)smem;
+  lds_ptr lds = (lds_ptr)smem + group_id<S>() * S::kGroupLds;
   constexpr int kSize = S::FP8 ? 1 : 2;
   constexpr int kCols = GLU ? S::BJ / 2 : S::BJ;  // columns of y in a tile
   constexpr int kWaveCols = kCols / S::WJ;        // and in a wave
@@ -56,7 +56,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void forward_kernel(
   if constexpr (S::FP8) {
     // the scales of a tile's weights: its gate and its up block, or its
     // 128-column blocks
-    const int tid = threadIdx.x;
+    const int tid = group_thread<S>();
     feed.s.init(blocks, tid < (GLU ? 2 : (S::BJ + 127) / 128) ? (GLU ? tid * (g.n / 128) : tid) : kNowhere);
   }
   auto source = [&](const RowTile &r) {
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void forward_kernel(
       s.w = {g.w_scales + (static_cast<int64_t>(r.e) * (wrows / 128) + j0 / 128) * blocks,
              wrows / 128 - j0 / 128};
     }
-    s.steps = (row_bytes + kStepBytes - 1) / kStepBytes;
+    s.steps = (row_bytes + kStepBytes * S::WK - 1) / (kStepBytes * S::WK);
     return s;
   };
   auto scale_j = [&](int b) { return GLU ? b & 1 : (w.wj * S::FJ + b) * 16 / 128; };
@@ -86,6 +86,24 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void forward_kernel(
     f32x4 acc[FI][S::FJ];
     multiply<S, FI>(lds, feed, cur, following, at, scale_j, acc);
     const int lane = late_lane_id();
+    if constexpr (S::WK > 1) {
+      // the groups' sums, added in order by the first, through what is its way out
+      lds_ptr sums = lds + S::NST * S::kStage + lane * 16;
+      if (group_id<S>() > 0) {
+#pragma unroll
+        for (int b = 0; b < S::FJ; ++b) *(MOE_LDS f32x4 *)(sums + b * kWave * 16) = acc[0][b];
+      }
+      __syncthreads();
+      if (group_id<S>() > 0) {
+        at.younger = 0;
+        return;
+      }
+#pragma unroll
+      for (int q = 1; q < S::WK; ++q)
+#pragma unroll
+        for (int b = 0; b < S::FJ; ++b)
+          acc[0][b] += *(MOE_LDS const f32x4 *)(sums + q * S::kGroupLds + b * kWave * 16);
+    }
     const auto turn = Transpose<kTurnCols>::template make<S>(lds, lane);
     const float *bias = g.bias ? g.bias + static_cast<int64_t>(t.e) * wrows : nullptr;
     const int col0 = t.j * kCols + w.wj * kWaveCols;  // of the wave
@@ -189,7 +207,7 @@ hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream, int
   const int64_t tiles = row_tile_bound<S::BI>(pairs, g.n_experts) * g.col_tiles;
   const uint32_t grid = tile_grid(tiles, resident);
   return with_act(act, [&](auto a) {
-    forward_kernel<S, GLU, decltype(a)::value><<<grid, S::kThreads, 0, stream>>>(g);
+    forward_kernel<S, GLU, decltype(a)::value><<<grid, S::kThreads * S::WK, 0, stream>>>(g);
     return hipGetLastError();
   });
 }
@@ -197,10 +215,18 @@ hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream, int
 // Which tile, by the rows an expert has on average and by whether larger tiles would
 // leave compute units without work.  Measured at K = 4096, F = 1024 (gated, 64
 // experts, top 6; us a call, bf16 unless FP8 is said):
-//   rows an expert    0.1     0.75    4      64     96    128    192
-//   16 x 64           21.2   115.5  187.1   420.6  586.1  748.8 1038.9
-//   128 x 128         54.0   145.0  181.9   192.6  205.8  310.8  315.8
-//   256 x 256         72.3   165.6  193.3   211.1  224.2  235.6  268.9
+//   rows an expert       0.1     0.75    4      64     96    128    192
+//   16 x 64, K in four   18.2   105.6  178.4   393.9
+//   16 x 64              21.2   115.5  187.1   420.6  586.1  748.8 1038.9
+//   128 x 128            54.0   145.0  181.9   192.6  205.8  310.8  315.8
+//   256 x 256            72.3   165.6  193.3   211.1  224.2  235.6  268.9
+// A long contraction is split over the four waves of a 16 x 64 tile, for few rows an
+// expert (12 rows: 181.0 against 181.9 of 128 x 128, FP8 102.6 against 124.2; 16:
+// 192.2 against 181.9) and for few tiles, whose time is that of one chain of steps
+// (1 expert of 40 rows, K = 4096, F = 512: 10.5 against 23.3; 512 tiles, K = 7168:
+// 29.3 against 38.7; 528 tiles, K = 2048: 16.9 against 14.3).  A short one is not
+// worth the join (linear, 64 experts of 1 row, K = 2048: 120.4 against 125.0; K = 1024,
+// 0.4 rows: 38.9 against 36.8).
 // FP8 stays with 128 x 128: a 256 x 256 tile's sums, operands and block products
 // do not fit the registers.  With many rows its workgroups take one tile each, so that
 // tiles which share weights start together (K = 7168, F = 2048, 256 experts of
@@ -209,12 +235,16 @@ hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream, int
 // (1295 against 1204 us at 4 rows).
 template <bool GLU, bool FP8>
 hipError_t launch_sized(const ForwardArgs &g, int64_t pairs, int act, hipStream_t stream) {
+  typedef Shape<16, 64, 1, 1, 3, false, false, FP8, 4> Split;
   typedef Shape<16, 64, 1, 1, 6, false, false, FP8> Few;
   typedef Shape<64, 128, 2, 2, 3, false, false, FP8> Low;
   typedef Shape<128, 128, 2, 2, 2, false, false, FP8> Some;
   const int64_t used = pairs < g.n_experts ? pairs : g.n_experts, rows = (pairs + used - 1) / used;
   const int wrows = g.n * (GLU ? 2 : 1);
   const int64_t tiles = row_tile_bound<Some::BI>(pairs, g.n_experts) * col_tiles<Some::BJ>(wrows);
+  const int64_t split_tiles = row_tile_bound<Split::BI>(pairs, g.n_experts) * col_tiles<Split::BJ>(wrows);
+  if (g.k >= 2048 && (rows <= 12 || split_tiles <= 2 * kComputeUnits))
+    return launch<Split, GLU>(g, pairs, act, stream);
   if (rows <= 16 && tiles < 4 * kComputeUnits) return launch<Few, GLU>(g, pairs, act, stream);
   if (tiles < kEnoughTiles) return launch<Low, GLU>(g, pairs, act, stream);
   if (rows <= 112) return launch<Some, GLU>(g, pairs, act, stream);

@@ -56,13 +56,15 @@ constexpr uint32_t kNowhere = 0x80000000u;
 constexpr uint32_t kRecords = 0x7FFFFFFFu;
 
 // WI x WJ waves; each owns FI x FJ blocks of 16 x 16.  XI/XJ: the operand is
-// stored across c.  FP8: E4M3 codes (along c only) with block scales.
+// stored across c.  FP8: E4M3 codes (along c only) with block scales.  WK: such
+// groups of waves in a workgroup; each takes every WK-th step through stages of its
+// own, and the first adds up their sums (operands along c only).
 template <int BI_, int BJ_, int WI_, int WJ_, int NST_, bool XI_ = false, bool XJ_ = false,
-          bool FP8_ = false>
+          bool FP8_ = false, int WK_ = 1>
 struct Shape {
-  static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_;
+  static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_, WK = WK_;
   static constexpr bool XI = XI_, XJ = XJ_, FP8 = FP8_;
-  static constexpr int kThreads = WI * WJ * kWave;
+  static constexpr int kThreads = WI * WJ * kWave;  // of a group; a workgroup has WK
   static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
   // 16-byte loads a thread makes for an operand in a step; a tile smaller than one load
   // of every thread still gets a whole one (its spare rows are zeros)
@@ -74,26 +76,42 @@ struct Shape {
   static constexpr int kStage = kBytesI + kBytesJ + 2 * kBytesScale;
   // the results' way out: see Transpose.  FP8's larger stages leave room for half
   static constexpr int kWaveCols = BJ / WJ;
-  static constexpr int kTurnCols = FP8 && kWaveCols > 32 ? 32 : kWaveCols;
-  static constexpr int kLdsBytes = NST * kStage + WI * WJ * 16 * kTurnCols * 4;
+  static constexpr int kTurnCols = FP8 && WK == 1 && kWaveCols > 32 ? 32 : kWaveCols;
+  static constexpr int kGroupLds = NST * kStage + WI * WJ * 16 * kTurnCols * 4;
+  static constexpr int kLdsBytes = WK * kGroupLds;
   // workgroups that a compute unit holds: LDS, and two waves a SIMD
-  static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (WI * WJ);
+  static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (WI * WJ * WK);
   static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
   // Two waves a SIMD also keep the accumulators in the 256 registers that both
   // operands and results of an MFMA can name (with more, the compiler moves them to
   // and from the accumulation registers in the loop).  Small tiles with many
   // stages are held to one by their LDS.
-  static constexpr int kWavesPerSimd = kResident * WI * WJ >= 8 ? 2 : 1;
+  static constexpr int kWavesPerSimd = kResident * WI * WJ * WK >= 8 ? 2 : 1;
   static constexpr int kLoads = LI + LJ + (FP8 ? 2 : 0);  // of a wave and stage
   static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
   static_assert(kLoads * (NST - 1) < 64, "the wait counter holds 63 loads");
   static_assert(kLdsBytes <= 160 * 1024, "LDS of a compute unit");
+  static_assert(WK == 1 || (WI == 1 && WJ == 1 && FI == 1 && !XI && !XJ), "a group is one wave, its tile 16 rows");
 };
 
 // -------------------------------------------------------------- loaders ---
 
 __device__ __forceinline__ int wave_id() {
   return __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+}
+
+// A group's number, and a thread's and wave's number within it.
+template <class S>
+__device__ __forceinline__ int group_id() {
+  return S::WK == 1 ? 0 : wave_id() / (S::WI * S::WJ);
+}
+template <class S>
+__device__ __forceinline__ int group_thread() {
+  return S::WK == 1 ? threadIdx.x : threadIdx.x % S::kThreads;
+}
+template <class S>
+__device__ __forceinline__ int group_wave() {
+  return S::WK == 1 ? wave_id() : wave_id() % (S::WI * S::WJ);
 }
 
 // A buffer resource in the four scalar registers that an instruction names.
@@ -163,8 +181,8 @@ struct Along {
 
   __device__ __forceinline__ void init(int bytes) {
     row_bytes = bytes;
-    const int r = threadIdx.x / 8;
-    chunk = ((threadIdx.x & 7) ^ (r & 7)) * 16;
+    const int r = group_thread<S>() / 8;
+    chunk = ((group_thread<S>() & 7) ^ (r & 7)) * 16;
     off = row(r) * bytes + chunk;
   }
   __device__ __forceinline__ void issue(lds_ptr to, const Operand &o, int step) const {
@@ -173,8 +191,8 @@ struct Along {
     uint32_t place[L];
 #pragma unroll
     for (int u = 0; u < L; ++u) place[u] = first + row(u * S::kLoadRows) * row_bytes;
-    load_lds16<S::kThreads * 16>(resource(o.base + at, max(o.extent - at, 0)), to + wave_id() * kWave * 16,
-                                 place);
+    load_lds16<S::kThreads * 16>(resource(o.base + at, max(o.extent - at, 0)),
+                                 to + group_wave<S>() * kWave * 16, place);
   }
 };
 struct SameRow {
@@ -230,11 +248,11 @@ struct ScaleLanes {
   // the tile's first, or kNowhere
   __device__ __forceinline__ void init(int n, uint32_t weight_row) {
     blocks = n;
-    row_off = threadIdx.x < S::BI ? threadIdx.x * n * 4 : kNowhere;
+    row_off = group_thread<S>() < S::BI ? group_thread<S>() * n * 4 : kNowhere;
     weight_off = weight_row == kNowhere ? kNowhere : weight_row * n * 4;
   }
   __device__ __forceinline__ void issue(lds_ptr to, const Scales &x, const Scales &w, int step) const {
-    to += wave_id() * kWave * 4;
+    to += group_wave<S>() * kWave * 4;
     load_lds4(resource(x.base + step, bytes(x, step)), to, row_off);
     load_lds4(resource(w.base + step, bytes(w, step)), to + S::kBytesScale, weight_off);
   }
@@ -277,6 +295,7 @@ struct Feed {
   LS s;
   __device__ __forceinline__ void issue(lds_ptr lds, int stage, const Source &src, int step) const {
     lds_ptr to = lds + stage * S::kStage;
+    if constexpr (S::WK > 1) step = step * S::WK + group_id<S>();
     i.issue(to, src.i, step);
     j.issue(to + S::kBytesI, src.j, step);
     if constexpr (S::FP8) s.issue(to + S::kBytesI + S::kBytesJ, src.x, src.w, step);
@@ -354,7 +373,7 @@ struct Wave {
 };
 template <class S>
 __device__ __forceinline__ Wave<S> this_wave() {
-  const int w = wave_id();
+  const int w = group_wave<S>();
   return {w / S::WJ, w % S::WJ};
 }
 
@@ -518,7 +537,7 @@ struct Transpose {
   // of this wave, behind the stages
   template <class S>
   __device__ __forceinline__ static Transpose make(lds_ptr lds, int lane) {
-    return {lds + S::NST * S::kStage + wave_id() * kBytes, lane};
+    return {lds + S::NST * S::kStage + group_wave<S>() * kBytes, lane};
   }
   static constexpr int kChunks = COLS / 4;
   static constexpr int kBytes = 16 * COLS * 4;

@@ -82,6 +82,12 @@ SIZES = [
     dict(tokens=2500, experts=3, top_k=1, k=776, f=1032, bias=True),
     dict(tokens=2000, experts=8, top_k=2, k=1400, f=1552, masked=0.05, skew=0.3, act="gelu_tanh", bias=True),
     dict(tokens=1100, experts=64, top_k=6, k=1032, f=264, pad=16),
+    # a long contraction with few rows an expert or few tiles: split over the waves, with
+    # uneven shares, and with more tiles than workgroups
+    dict(tokens=1, experts=4, top_k=1, k=2048, f=24),
+    dict(tokens=70, experts=5, top_k=2, k=2120, f=136, masked=0.1, act="gelu_tanh", bias=True),
+    dict(tokens=500, experts=1, top_k=1, k=2056, f=264),
+    dict(tokens=160, experts=96, top_k=6, k=2304, f=200, pad=16, skew=0.5, bias=True),
 ]
 
 
@@ -139,6 +145,10 @@ FP8_SIZES = [
     # enough tiles: workgroups that take tile after tile, and one workgroup a tile
     dict(tokens=300, experts=64, top_k=6, k=384, f=256, pad=16, bias=True),
     dict(tokens=3000, experts=4, top_k=1, k=512, f=768, skew=0.5, bias=True),
+    # split over the waves: uneven shares of the steps, more tiles than workgroups
+    dict(tokens=3, experts=2, top_k=2, k=2048, f=256, bias=True),
+    dict(tokens=200, experts=40, top_k=2, k=2176, f=384, masked=0.1),
+    dict(tokens=40, experts=2, top_k=2, k=2432, f=128, act="none", bias=True),
 ]
 
 
