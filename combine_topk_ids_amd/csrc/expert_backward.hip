@@ -294,7 +294,8 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
     multiply<S, S::FI>(lds, feed, cur, following, at, [](int) { return 0; }, acc);
     const int64_t row = static_cast<int64_t>(PARTS ? t.part * g.n_experts + t.e : t.e) * g.n + t.i0;
     if constexpr (PARTS)
-      at.younger = store_tile<S, S::FI, kLoadDefault>(lds, acc, g.parts + row * g.k + t.j0, g.k, g.n - t.i0, g.k - t.j0);
+      at.younger = store_tile<S, S::FI, kLoadDefault>(lds, acc, g.parts + row * g.k + t.j0, g.k, g.n - t.i0,
+                                                      g.k - t.j0);
     else
       // streaming: nobody reads dw soon (64 experts, 2048 x 4096: the next call's dz then
       // takes 43 us, not 65, while 1 GB of dw need not be written back first)
