@@ -20,7 +20,7 @@ using namespace tile;
 // rows: 15.1 us against 7.2 at 999 rows of 2 x 712 columns, 70.2 against 66.8 at 24576
 // of 2 x 1024.)
 constexpr int kChunkRows = kBiasChunkRows;
-constexpr int kSlabCols = 512;   // columns of a workgroup: 8 a lane
+constexpr int kSlabCols = kGradCols;  // columns of a workgroup: 8 a lane
 constexpr int kWaves = 4;
 constexpr int kBatch = 4;
 
@@ -129,13 +129,13 @@ __global__ __launch_bounds__(256) void bias_kernel(GradArgs g, float *dbias) {
 }
 
 template <bool GLU>
-hipError_t launch_grad(GradArgs g, int64_t pairs, int act, hipStream_t stream) {
+hipError_t launch_grad(GradArgs g, int64_t groups, int act, hipStream_t stream) {
+  static_assert(kSlabCols == 8 * kWave && kWaves * kWave == kGradThreads, "the launch that the checks bound");
   g.col_tiles = (g.n + kSlabCols - 1) / kSlabCols;
-  const int64_t tiles = row_tile_bound<kChunkRows>(pairs, g.n_experts) * g.col_tiles;
-  if (tiles == 0) return hipSuccess;
+  if (groups == 0) return hipSuccess;
   return with_act(act, [&](auto a) {
     grad_kernel<GLU, decltype(a)::value>
-        <<<static_cast<uint32_t>((tiles + 7) / 8 * 8), kWaves * kWave, 0, stream>>>(g);
+        <<<static_cast<uint32_t>(groups), kWaves * kWave, 0, stream>>>(g);
     return hipGetLastError();
   });
 }
@@ -403,7 +403,8 @@ hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, co
     g.rows = static_cast<int>(max_rows(p));
     g.n = op.out_dim;
     g.width = width;
-    err = glu ? launch_grad<true>(g, pairs, op.act, stream) : launch_grad<false>(g, pairs, op.act, stream);
+    const int64_t groups = expert_grad_workgroups(p, op.out_dim);
+    err = glu ? launch_grad<true>(g, groups, op.act, stream) : launch_grad<false>(g, groups, op.act, stream);
     if (err != hipSuccess) return err;
     if (b.dbias) {
       bias_kernel<<<dim3((width + 15) / 16, p.n_experts), 256, 0, stream>>>(g, b.dbias);

@@ -122,6 +122,12 @@ int dw_parts(const moe_problem &p, int64_t n, int64_t k) {
   return parts > 1 ? static_cast<int>(parts) : 1;
 }
 
+int64_t expert_grad_workgroups(const moe_problem &p, int64_t out_dim) {
+  const int64_t pairs = expert_row_bound(p), used = pairs < p.n_experts ? pairs : p.n_experts;
+  const int64_t chunks = (pairs + used * (kBiasChunkRows - 1)) / kBiasChunkRows;
+  return (chunks * ((out_dim + kGradCols - 1) / kGradCols) + 7) / 8 * 8;
+}
+
 size_t expert_bias_bytes(const moe_problem &p, const moe_expert_op &op) {
   const size_t chunks = static_cast<size_t>(max_rows(p)) / kBiasChunkRows + p.n_experts + 1;
   return align256(chunks * 2 * static_cast<size_t>(op.out_dim) * sizeof(float));
@@ -407,9 +413,12 @@ int check_expert_op(const moe_problem *p, const moe_expert_op *op) {
   // in a tile of 256 rows fit the kernels' 31-bit buffer offsets
   const int64_t in = op->in_dim, out = op->out_dim;
   if (in > (1 << 20) || out > (1 << 20) || in * out >= (int64_t{1} << 29)) return MOE_EOVERFLOW;
-  // a launch has one workgroup per tile of at least 64 rows (or one per expert) by 64 columns
+  // tiles of the products, 64 rows (or an expert) by 64 columns: their numbers, also of
+  // 16-row tiles, fit int32, and one workgroup of 256 threads for each fits a launch
   const int64_t wide = (in > 2 * out ? in : 2 * out) / 64 + 1;
   if ((expert_row_bound(*p) / 64 + p->n_experts) * wide >= (int64_t{1} << 22)) return MOE_EOVERFLOW;
+  // a launch's threads fit uint32 in each dimension: dz's are the most
+  if (expert_grad_workgroups(*p, out) * kGradThreads > UINT32_MAX) return MOE_EOVERFLOW;
   return MOE_OK;
 }
 

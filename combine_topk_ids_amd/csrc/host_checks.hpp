@@ -100,6 +100,10 @@ int dw_parts(const moe_problem &p, int64_t n, int64_t k);
 // chunks of each expert (at most rows / 16 + E of them, up to 2 * out_dim
 // columns), for dbias; then the parts of dw, fp32.
 constexpr int kBiasChunkRows = 16;
+// The launch that computes dz (of a layer's out_dim columns): one workgroup for
+// every such chunk, of any routing, and kGradCols columns, in whole rounds of the 8 XCDs.
+constexpr int kGradCols = 512, kGradThreads = 256;
+int64_t expert_grad_workgroups(const moe_problem &p, int64_t out_dim);
 size_t expert_bias_bytes(const moe_problem &p, const moe_expert_op &op);
 size_t expert_workspace_bytes(const moe_problem &p, const moe_expert_op &op);
 

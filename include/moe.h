@@ -375,8 +375,10 @@ MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
  * change while a call runs.
  *
  * p names the packed buffer (R_max rows, E experts); its hidden and fmt are not
- * used here.  Needs in_dim, out_dim <= 2^20, in_dim * out_dim < 2^29 and
- * (rows / 64 + E) * max(in_dim, 2 * out_dim) / 64 < 2^22 (MOE_EOVERFLOW). */
+ * used here.  Needs, with R the rows that can hold a token (N * k, or R_max if that
+ * is less), in_dim, out_dim <= 2^20, in_dim * out_dim < 2^29, (R / 64 + E) *
+ * (max(in_dim, 2 * out_dim) / 64 + 1) < 2^22 and, for the 16-row workgroups of
+ * dz, (R + 15 * E) / 16 <= 2^24 - 8 (MOE_EOVERFLOW). */
 typedef enum moe_act {
   MOE_ACT_NONE = 0,
   MOE_ACT_SILU = 1,      /* z * sigmoid(z)                                    */
