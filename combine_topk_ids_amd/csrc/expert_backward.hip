@@ -297,8 +297,12 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
       at.younger = store_tile<S, S::FI, kLoadDefault>(lds, acc, g.parts + row * g.k + t.j0, g.k, g.n - t.i0,
                                                       g.k - t.j0);
     else
-      // streaming: nobody reads dw soon (64 experts, 2048 x 4096: the next call's dz then
-      // takes 43 us, not 65, while 1 GB of dw need not be written back first)
+      // streaming: what follows need not wait for dw to be written back (64 experts, 2048 x
+      // 4096, 1 GB: 507 us against 538 for ordinary stores, and the next call's dz takes
+      // 43 us, not 65; 256 MB: 113 against 142).  A reader right behind pays for it where dw
+      // would have stayed in the caches, at most what it saves elsewhere (with m += c dw:
+      // 16 MB 19.9 against 22.2 us, 64 MB 53.2 / 50.8, 128 MB 131.9 / 129.8, 256 MB 270 / 277,
+      // 1 GB 1042 / 1078).
       at.younger =
           store_tile<S, S::FI, kLoadNT>(lds, acc, g.out + row * g.k + t.j0, g.k, g.n - t.i0, g.k - t.j0);
     t = next;
@@ -359,6 +363,10 @@ hipError_t launch_dx_sized(const ProductArgs &g, int64_t pairs, hipStream_t stre
   typedef Shape<256, 256, 2, 4, 2, false, true> Large;
   typedef Shape<128, 128, 2, 2, 2, false, true> Middle;
   typedef Shape<64, 128, 2, 2, 4, false, true> Small;
+  // (Rounds of 256 workgroups, 256 x 256 against 128 x 128 tiles, us: 1.5 rounds, 24 experts
+  // of 256 rows, K = 4096, N = 1024, 65.4 / 62.0, 12 of 1024, K = N = 2048, 103.9 / 99.1;
+  // 2.0 rounds 77.0 / 94.4; 2.1 99.2 / 100.8; 3.5 139.5 / 155.3; 8, 64 experts of 384 rows,
+  // K = 4096, N = 2048, 416 / 448.  Fewer: at kEnoughTiles.)
   if (row_tile_bound<Large::BI>(pairs, g.n_experts) * col_tiles<Large::BJ>(g.k) >= kEnoughTiles)
     return launch_dx<Large>(g, pairs, stream);
   if (row_tile_bound<Middle::BI>(pairs, g.n_experts) * col_tiles<Middle::BJ>(g.k) >= kEnoughTiles)
@@ -368,7 +376,10 @@ hipError_t launch_dx_sized(const ProductArgs &g, int64_t pairs, hipStream_t stre
 
 // (2N = K = 1024: 8 experts, 128 tiles of 256 x 256, 31.6 us, of 128 x 128, 22.3;
 // 16 experts, 256 tiles, 12.8 and 13.3; 2 experts with 2N = 512, K = 256 and 8192 rows,
-// 16 tiles of 128 x 128, 79.7, of 64 x 64, 49.5.)
+// 16 tiles of 128 x 128, 79.7, of 64 x 64, 49.5.  The rows an expert has do not move the
+// border, 256 x 256 / 128 x 128: 64 experts, 4096 x 2048, 64 rows 233 / 259, 128 rows 241 /
+// 264, 384 rows 507 / 565, 1024 rows 1024 / 1215; 16 experts, 2048 x 2048, 256 tiles of
+// 256 x 256: 37.0 / 35.7, 37.1 / 37.0, 65.4 / 65.1, 128.9 / 139.4.)
 hipError_t launch_dw_sized(const ProductArgs &g, int parts, hipStream_t stream) {
   typedef Shape<256, 256, 2, 4, 2, true, true> Large;
   typedef Shape<128, 128, 2, 2, 2, true, true> Middle;

@@ -229,12 +229,22 @@ hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream, int
 // 29.3 against 38.7; 528 tiles, K = 2048: 16.9 against 14.3).  A short one is not
 // worth the join (linear, 64 experts of 1 row, K = 2048: 120.4 against 125.0; K = 1024,
 // 0.4 rows: 38.9 against 36.8).
+// The rows an expert has on average are all the host knows.  Where the routing sends
+// them all to a few experts, the tile picked for few rows is the wrong one (K = 4096,
+// F = 1024, bf16; 64 experts, 768 rows on six of them: K in four 50 us, 64 x 128
+// 25, 128 x 128 42; 256 experts, 3072 rows on six: 182, 69, 54; 6144 rows of 64 experts
+// on six: 128 x 128 97, 256 x 256 96).
 // FP8 stays with 128 x 128: a 256 x 256 tile's sums, operands and block products
 // do not fit the registers.  With many rows its workgroups take one tile each, so that
-// tiles which share weights start together (K = 7168, F = 2048, 256 experts of
-// 256 rows: 3158 us against 4231 for workgroups that take tile after tile, whose
-// L2 misses were 22.9 GB against 15.2); with few the weights pass once in any order
-// (1295 against 1204 us at 4 rows).
+// tiles which share weights start together: that pays for the largest weights and a
+// long contraction, and costs the run-on of the loads, and so time, elsewhere (gated, us,
+// one tile each against tile after tile; F = 2048, 256 rows an expert):
+//   K                 1024         2048         4096          7168
+//   8 experts      17.2 / 17.8  26.7 / 26.8  49.0 / 49.1   79.7 / 78.4
+//   64 experts      128 / 115    216 / 197    404 / 379     694 / 678
+//   256 experts     534 / 438    882 / 780   1563 / 1561   2748 / 3107
+// (L2 misses of the last: 15.2 GB against 22.9.)  With few rows the weights pass
+// once in any order (1295 against 1204 us at 4 rows).
 template <bool GLU, bool FP8>
 hipError_t launch_sized(const ForwardArgs &g, int64_t pairs, int act, hipStream_t stream) {
   typedef Shape<16, 64, 1, 1, 3, false, false, FP8, 4> Split;
