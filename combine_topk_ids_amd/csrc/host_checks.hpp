@@ -92,7 +92,14 @@ inline int64_t expert_row_bound(const moe_problem &p) {
 
 // Parts that the rows of an expert are split into for its weights' gradient
 // [E][n][k]: more than one where 64 x 64 tiles of it would leave most compute units
-// without work and the rows are many.  At most kDwWorkgroups workgroups.
+// without work and the rows are many.  At most kDwWorkgroups workgroups.  (us a call,
+// parts against whole, by the rows of an expert:
+//   rows                          1024           2048           8192
+//   1 expert, 128 x 128       11.9 / 10.0    11.8 / 15.1    13.8 / 51.1
+//   2 experts, 512 x 256      13.1 / 11.0    16.7 / 15.4    22.6 / 49.8
+//   8 experts, 256 x 256      15.7 / 10.2    16.7 / 15.8    31.1 / 53.1
+//   4 experts, 512 x 512      16.9 / 12.1    21.0 / 16.0    52.4 / 54.8 (two parts)
+// The launch that joins the parts costs 2 to 5 us: from some 2000 rows on they pay.)
 constexpr int kDwTile = 64, kDwWorkgroups = 512, kDwMostParts = 16, kDwPartRows = 256;
 int dw_parts(const moe_problem &p, int64_t n, int64_t k);
 

@@ -386,6 +386,9 @@ MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
  * row or expert only.  Outputs must not overlap inputs or each other (but the
  * residual may be y itself); the plan must not change while a call runs.
  *
+ * The exchange's receive buffers (source-major: an expert's rows are one run per
+ * source) are not covered.
+ *
  * p names the packed buffer (R_max rows, E experts); its hidden and fmt are not
  * used here.  Needs, with R the rows that can hold a token (N * k, or R_max if that
  * is less), in_dim, out_dim <= 2^20, in_dim * out_dim < 2^29, (R / 64 + E) *
