@@ -372,8 +372,8 @@ MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
  * are stored.  With FP8 operands the 128 products of a scale block are added by the
  * FP8 matrix instruction, which keeps fewer bits of the small ones: with E the largest sum of
  * two codes' exponents among eight neighbouring columns (8i .. 8i+7), their
- * products are cut towards zero to multiples of 2^(E-13); the blocks' sums are scaled and
- * added in fp32.
+ * products are cut towards zero to multiples of 2^(E-13); the blocks' sums are
+ * multiplied by fl32(x_scale * w_scale) and added in fp32.
  *
  * Runs repeat bit for bit.  For one moe_problem and moe_expert_op the bits of a
  * row's results (z, h, y, dz, dx) depend on that row, its expert's weights and its bias
