@@ -299,9 +299,9 @@ __global__ __launch_bounds__(S::kThreads, S::kWavesPerSimd) void dw_kernel(Produ
     else
       // streaming: what follows need not wait for dw to be written back (64 experts, 2048 x
       // 4096, 1 GB: 507 us against 538 for ordinary stores, and the next call's dz takes
-      // 43 us, not 65; 256 MB: 113 against 142).  A reader right behind pays for it where dw
-      // would have stayed in the caches, at most what it saves elsewhere (with m += c dw:
-      // 16 MB 19.9 against 22.2 us, 64 MB 53.2 / 50.8, 128 MB 131.9 / 129.8, 256 MB 270 / 277,
+      // 43 us, not 65; 256 MB: 113 against 142).  With a reader right behind, which might
+      // have found dw in the caches, from 10% faster to 5% slower (m += c dw behind it,
+      // 16 MB: 19.9 against 22.2 us, 64 MB 53.2 / 50.8, 128 MB 131.9 / 129.8, 256 MB 270 / 277,
       // 1 GB 1042 / 1078).
       at.younger =
           store_tile<S, S::FI, kLoadNT>(lds, acc, g.out + row * g.k + t.j0, g.k, g.n - t.i0, g.k - t.j0);

@@ -439,7 +439,7 @@ __device__ __forceinline__ void multiply(lds_ptr lds, const F &feed, const Sourc
     // the largest: with E the largest sum of the two codes' exponents among them (a
     // subnormal code's is -6), each is cut towards zero to a multiple of 2^(E-13), so
     // a group is off by less than 7 * 2^(E-13).  (Measured, for this form and the
-    // 32-deep one.  Codes of normal values: at most 2^-15.5 of the sum of magnitudes; z over
+    // 32-deep one.  A block of normal values: at most 2^-15 of the sum of magnitudes; h over
     // K = 7168, once rounded to bf16, differs from an fp32 evaluation by 2.8e-4, against 1.7e-3
     // for that rounding itself.)  Codes converted to bf16, which holds them exactly, would keep
     // 2^-23, at the bf16 rate (library products of 8192^3: 1457 TFLOP/s against 3150).  A
@@ -746,6 +746,9 @@ inline int64_t row_tile_bound(int64_t pairs, int n_experts) {
 
 // ---------------------------------------------------------- activations ---
 
+// The hardware's exp2 and reciprocal, a unit in the last place each: off by (|z| + 8) 2^-23
+// of its value, which the rounding to bf16 hides.  Below 2^-126 it is zero: an
+// activation of z < -87 comes out as -0 where its value is less than |z| 2^-126.
 __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.0f + __expf(-z)); }
 
 // value and slope of an activation (a moe_act)

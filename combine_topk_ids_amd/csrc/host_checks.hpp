@@ -99,7 +99,8 @@ inline int64_t expert_row_bound(const moe_problem &p) {
 //   2 experts, 512 x 256      13.1 / 11.0    16.7 / 15.4    22.6 / 49.8
 //   8 experts, 256 x 256      15.7 / 10.2    16.7 / 15.8    31.1 / 53.1
 //   4 experts, 512 x 512      16.9 / 12.1    21.0 / 16.0    52.4 / 54.8 (two parts)
-// The launch that joins the parts costs 2 to 5 us: from some 2000 rows on they pay.)
+// The launch that joins the parts costs 2 to 5 us, which the split
+// earns back somewhere between 2000 and 8000 rows, and before in the smallest dw.)
 constexpr int kDwTile = 64, kDwWorkgroups = 512, kDwMostParts = 16, kDwPartRows = 256;
 int dw_parts(const moe_problem &p, int64_t n, int64_t k);
 
