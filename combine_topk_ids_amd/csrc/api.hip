@@ -324,6 +324,58 @@ MOE_API int moe_expert_linear_backward(const moe_problem *p, const moe_plan *pla
                                               static_cast<hipStream_t>(stream)));
 }
 
+MOE_API int moe_check_router(const moe_problem *p, const moe_router *r) { return check_router(p, r); }
+
+MOE_API int moe_route(const moe_problem *p, const moe_router *r, const void *logits, const float *bias,
+                      int32_t *topk_ids, float *topk_weights, float *scores, void *stream) {
+  const int rc = check_route_args(p, r, logits, bias, topk_ids, topk_weights, scores);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_route(*p, *r, logits, bias, topk_ids, topk_weights, scores,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_route_backward(const moe_problem *p, const moe_router *r, const void *logits,
+                               const int32_t *topk_ids, const float *dweights, const float *dscores,
+                               void *dlogits, void *stream) {
+  const int rc = check_route_backward_args(p, r, logits, topk_ids, dweights, dscores, dlogits);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_route_backward(*p, *r, logits, topk_ids, dweights, dscores, dlogits,
+                                             static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_quantize_mxfp4(int64_t rows, int32_t cols, const uint16_t *x, uint8_t *codes,
+                               uint8_t *scales, void *stream) {
+  const int rc = check_quantize_args(rows, cols, x, codes, scales);
+  if (rc != MOE_OK) return rc;
+  return launched(
+      moe::launch_quantize_mxfp4(rows * cols, x, codes, scales, static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_check_expert_mx_op(const moe_problem *p, const moe_expert_op *op) {
+  return check_expert_mx_op(p, op);
+}
+
+MOE_API int moe_expert_glu_mx(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                              const void *x, const void *x_scales, const uint8_t *w, const uint8_t *w_scales,
+                              const float *bias, void *h, uint8_t *h_scales, void *stream) {
+  const int rc = check_expert_mx_args(p, plan, op, x, x_scales, w, w_scales, bias, nullptr, h, h_scales);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_expert_mx(*p, *plan, *op, true,
+                                        {x, x_scales, w, w_scales, bias, nullptr, h, h_scales},
+                                        static_cast<hipStream_t>(stream)));
+}
+
+MOE_API int moe_expert_linear_mx(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                                 const void *x, const void *x_scales, const uint8_t *w,
+                                 const uint8_t *w_scales, const float *bias, const uint16_t *residual,
+                                 uint16_t *y, void *stream) {
+  const int rc = check_expert_mx_args(p, plan, op, x, x_scales, w, w_scales, bias, residual, y, nullptr);
+  if (rc != MOE_OK) return rc;
+  return launched(moe::launch_expert_mx(*p, *plan, *op, false,
+                                        {x, x_scales, w, w_scales, bias, residual, y, nullptr},
+                                        static_cast<hipStream_t>(stream)));
+}
+
 MOE_API const char *moe_strerror(int code) { return error_text(code); }
 
 }  // extern "C"

@@ -5,6 +5,8 @@
 
 #include <math.h>
 
+#include <cmath>
+
 namespace moe {
 namespace {
 
@@ -401,14 +403,8 @@ int check_combine_backward_args(const moe_problem *p, const moe_plan *plan, cons
   return MOE_OK;
 }
 
-int check_expert_op(const moe_problem *p, const moe_expert_op *op) {
-  const int rc = check_problem(p);
-  if (rc != MOE_OK) return rc;
-  if (!op) return MOE_EINVAL;
-  const int unit = op->fmt == MOE_FMT_BF16 ? 8 : 128;  // a 16-byte row unit, or a scale block
-  if (op->fmt != MOE_FMT_BF16 && op->fmt != MOE_FMT_FP8_E4M3_B128) return MOE_EINVAL;
-  if (op->in_dim <= 0 || op->out_dim <= 0 || op->in_dim % unit || op->out_dim % unit) return MOE_EINVAL;
-  if (op->act < MOE_ACT_NONE || op->act > MOE_ACT_RELU) return MOE_EINVAL;
+// what the products of every format need of a layer's sizes
+static int check_expert_sizes(const moe_problem *p, const moe_expert_op *op) {
   // byte offsets in one expert's weights (up to 2 * out_dim rows of bf16) and
   // in a tile of 256 rows fit the kernels' 31-bit buffer offsets
   const int64_t in = op->in_dim, out = op->out_dim;
@@ -420,6 +416,17 @@ int check_expert_op(const moe_problem *p, const moe_expert_op *op) {
   // a launch's threads fit uint32 in each dimension: dz's are the most
   if (expert_grad_workgroups(*p, out) * kGradThreads > UINT32_MAX) return MOE_EOVERFLOW;
   return MOE_OK;
+}
+
+int check_expert_op(const moe_problem *p, const moe_expert_op *op) {
+  const int rc = check_problem(p);
+  if (rc != MOE_OK) return rc;
+  if (!op) return MOE_EINVAL;
+  const int unit = op->fmt == MOE_FMT_BF16 ? 8 : 128;  // a 16-byte row unit, or a scale block
+  if (op->fmt != MOE_FMT_BF16 && op->fmt != MOE_FMT_FP8_E4M3_B128) return MOE_EINVAL;
+  if (op->in_dim <= 0 || op->out_dim <= 0 || op->in_dim % unit || op->out_dim % unit) return MOE_EINVAL;
+  if (op->act < MOE_ACT_NONE || op->act > MOE_ACT_RELU) return MOE_EINVAL;
+  return check_expert_sizes(p, op);
 }
 
 int check_expert_forward_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
@@ -457,6 +464,84 @@ int check_expert_backward_args(const moe_problem *p, const moe_plan *plan, const
   if (!aligned(dy, 16) || !aligned(preact, 16) || !aligned(x, 16) || !aligned(w, 16) || !aligned(dz, 16) ||
       !aligned(dx, 16) || !aligned(dw, 16) || !aligned(dbias, 4) || !aligned(workspace, 256) ||
       !aligned(plan->expert_counts, 4) || !aligned(plan->expert_offsets, 4))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_router(const moe_problem *p, const moe_router *r) {
+  const int rc = check_problem(p);
+  if (rc != MOE_OK) return rc;
+  if (!r) return MOE_EINVAL;
+  if (r->score != MOE_SCORE_SOFTMAX && r->score != MOE_SCORE_SIGMOID) return MOE_EINVAL;
+  if (r->logits != MOE_LOGITS_F32 && r->logits != MOE_LOGITS_BF16) return MOE_EINVAL;
+  if (r->n_groups < 1 || p->n_experts % r->n_groups) return MOE_EINVAL;
+  if (r->top_groups < 1 || r->top_groups > r->n_groups) return MOE_EINVAL;
+  if (p->top_k > r->top_groups * (p->n_experts / r->n_groups)) return MOE_EINVAL;
+  if (r->group_top != 1 && r->group_top != 2) return MOE_EINVAL;
+  if (r->renormalize != 0 && r->renormalize != 1) return MOE_EINVAL;
+  if (!std::isfinite(r->scale)) return MOE_EINVAL;
+  return MOE_OK;
+}
+
+// alignment of a row of logits' first element
+static int logit_bytes(const moe_router &r) { return r.logits == MOE_LOGITS_BF16 ? 2 : 4; }
+
+int check_route_args(const moe_problem *p, const moe_router *r, const void *logits, const float *bias,
+                     const int32_t *topk_ids, const float *topk_weights, const float *scores) {
+  const int rc = check_router(p, r);
+  if (rc != MOE_OK) return rc;
+  if (p->n_tokens > 0 && (!logits || !topk_ids)) return MOE_EINVAL;
+  if (!aligned(logits, logit_bytes(*r)) || !aligned(bias, 4) || !aligned(topk_ids, 4) ||
+      !aligned(topk_weights, 4) || !aligned(scores, 4))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_route_backward_args(const moe_problem *p, const moe_router *r, const void *logits,
+                              const int32_t *topk_ids, const float *dweights, const float *dscores,
+                              const void *dlogits) {
+  const int rc = check_router(p, r);
+  if (rc != MOE_OK) return rc;
+  if (p->n_tokens > 0 && (!logits || !dlogits || (!dweights && !dscores) || (dweights && !topk_ids)))
+    return MOE_EINVAL;
+  if (!aligned(logits, logit_bytes(*r)) || !aligned(dlogits, logit_bytes(*r)) || !aligned(topk_ids, 4) ||
+      !aligned(dweights, 4) || !aligned(dscores, 4))
+    return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_quantize_args(int64_t rows, int32_t cols, const uint16_t *x, const uint8_t *codes,
+                        const uint8_t *scales) {
+  if (rows < 0 || cols <= 0 || cols % 32) return MOE_EINVAL;
+  if (rows >= (int64_t{1} << 46) / cols) return MOE_EOVERFLOW;
+  if (rows > 0 && (!x || !codes || !scales)) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(codes, 16)) return MOE_EALIGN;
+  return MOE_OK;
+}
+
+int check_expert_mx_op(const moe_problem *p, const moe_expert_op *op) {
+  const int rc = check_problem(p);
+  if (rc != MOE_OK) return rc;
+  if (!op) return MOE_EINVAL;
+  if (op->fmt != MOE_FMT_MXFP4_B32 && op->fmt != MOE_FMT_FP8_E4M3_B128) return MOE_EINVAL;
+  const int unit = op->fmt == MOE_FMT_MXFP4_B32 ? 32 : 128;  // a scale block of the rows
+  if (op->in_dim <= 0 || op->out_dim <= 0 || op->in_dim % unit || op->out_dim % 8) return MOE_EINVAL;
+  if (op->act < MOE_ACT_NONE || op->act > MOE_ACT_RELU) return MOE_EINVAL;
+  return check_expert_sizes(p, op);
+}
+
+int check_expert_mx_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                         const void *x, const void *x_scales, const uint8_t *w, const uint8_t *w_scales,
+                         const float *bias, const uint16_t *residual, const void *y,
+                         const uint8_t *y_scales) {
+  const int rc = check_expert_mx_op(p, op);
+  if (rc != MOE_OK) return rc;
+  if (!plan || !plan->expert_counts || !plan->expert_offsets) return MOE_EINVAL;
+  if (y_scales && op->out_dim % 32) return MOE_EINVAL;
+  if (expert_row_bound(*p) > 0 && (!x || !x_scales || !w || !w_scales || !y)) return MOE_EINVAL;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(y, 16) || !aligned(residual, 16) || !aligned(bias, 16) ||
+      !aligned(x_scales, 4) || !aligned(w_scales, 4) || !aligned(plan->expert_counts, 4) ||
+      !aligned(plan->expert_offsets, 4))
     return MOE_EALIGN;
   return MOE_OK;
 }

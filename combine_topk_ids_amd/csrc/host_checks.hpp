@@ -169,6 +169,22 @@ int check_expert_backward_args(const moe_problem *p, const moe_plan *plan, const
                                const uint16_t *w, const uint16_t *dz, const uint16_t *dx,
                                const uint16_t *dw, const float *dbias, const void *workspace);
 
+int check_router(const moe_problem *p, const moe_router *r);
+int check_route_args(const moe_problem *p, const moe_router *r, const void *logits, const float *bias,
+                     const int32_t *topk_ids, const float *topk_weights, const float *scores);
+int check_route_backward_args(const moe_problem *p, const moe_router *r, const void *logits,
+                              const int32_t *topk_ids, const float *dweights, const float *dscores,
+                              const void *dlogits);
+
+int check_quantize_args(int64_t rows, int32_t cols, const uint16_t *x, const uint8_t *codes,
+                        const uint8_t *scales);
+int check_expert_mx_op(const moe_problem *p, const moe_expert_op *op);
+// y_scales: the gated block only; residual: the linear layer only
+int check_expert_mx_args(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                         const void *x, const void *x_scales, const uint8_t *w, const uint8_t *w_scales,
+                         const float *bias, const uint16_t *residual, const void *y,
+                         const uint8_t *y_scales);
+
 const char *error_text(int code);
 
 }  // namespace host

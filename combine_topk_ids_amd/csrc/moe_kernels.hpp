@@ -92,4 +92,27 @@ struct ExpertBackward {
 hipError_t launch_expert_backward(const moe_problem &p, const moe_plan &plan, const moe_expert_op &op,
                                   bool glu, const ExpertBackward &b, hipStream_t stream);
 
+// Routing: IDs, gate weights and scores from logits; its gradient.
+hipError_t launch_route(const moe_problem &p, const moe_router &r, const void *logits, const float *bias,
+                        int32_t *ids, float *weights, float *scores, hipStream_t stream);
+hipError_t launch_route_backward(const moe_problem &p, const moe_router &r, const void *logits,
+                                 const int32_t *ids, const float *dweights, const float *dscores,
+                                 void *dlogits, hipStream_t stream);
+
+// bf16 rows to MX-FP4 codes and scale bytes (rows * cols values, whole blocks).
+hipError_t launch_quantize_mxfp4(int64_t values, const uint16_t *x, uint8_t *codes, uint8_t *scales,
+                                 hipStream_t stream);
+
+// The experts' products with MX-FP4 weights (glu: the gated block; y_scales: y is MX-FP4).
+struct ExpertMx {
+  const void *x, *x_scales;
+  const uint8_t *w, *w_scales;
+  const float *bias;
+  const uint16_t *residual;
+  void *y;
+  uint8_t *y_scales;
+};
+hipError_t launch_expert_mx(const moe_problem &p, const moe_plan &plan, const moe_expert_op &op, bool glu,
+                            const ExpertMx &f, hipStream_t stream);
+
 }  // namespace moe

@@ -25,6 +25,8 @@ STATUS_BAD_ID, STATUS_DUP_ID, STATUS_CAPACITY, STATUS_MAP_OVERFLOW, STATUS_DROPP
 STATUS_BAD_PLAN = 32
 FMT = {"bf16": 0, "fp8": 1, "mxfp4": 2, "nvfp4": 3}
 ACT = {"none": 0, "silu": 1, "gelu_tanh": 2, "relu": 3}
+SCORE = {"softmax": 0, "sigmoid": 1}
+LOGITS = {"fp32": 0, "bf16": 1}
 FLAG_ZERO_TAIL = 1
 # how moe_plan_and_dispatch runs a problem (moe_plan_and_dispatch_mode)
 PD_ONE_LAUNCH, PD_TILED, PD_SEPARATE = 1, 2, 3
@@ -41,6 +43,8 @@ EXPORTS = ("moe_check_problem", "moe_max_rows", "moe_expert_capacity", "moe_payl
            "moe_routing_map_to_topk", "moe_plan_and_dispatch_noalloc", "moe_combine_backward",
            "moe_check_expert_op", "moe_expert_workspace_bytes", "moe_expert_glu",
            "moe_expert_linear", "moe_expert_glu_backward", "moe_expert_linear_backward",
+           "moe_check_router", "moe_route", "moe_route_backward", "moe_quantize_mxfp4",
+           "moe_check_expert_mx_op", "moe_expert_glu_mx", "moe_expert_linear_mx",
            "moe_strerror")
 
 
@@ -74,6 +78,12 @@ class ExpertOp(ctypes.Structure):
     _fields_ = [(name, ctypes.c_int32) for name in ("in_dim", "out_dim", "act", "fmt")]
 
 
+class Router(ctypes.Structure):
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "score", "logits", "n_groups", "top_groups", "group_top", "renormalize")] + [
+        ("scale", ctypes.c_float)]
+
+
 def _load() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -81,7 +91,7 @@ def _load() -> ctypes.CDLL:
             "(there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, V = ctypes.POINTER(Problem), ctypes.c_void_p
-    L, O = ctypes.POINTER(Plan), ctypes.POINTER(ExpertOp)
+    L, O, R = ctypes.POINTER(Plan), ctypes.POINTER(ExpertOp), ctypes.POINTER(Router)
     sig = {
         "moe_check_problem": (ctypes.c_int, [P]),
         "moe_max_rows": (ctypes.c_int64, [P]),
@@ -116,6 +126,13 @@ def _load() -> ctypes.CDLL:
         "moe_expert_linear": (ctypes.c_int, [P, L, O] + [V] * 9),
         "moe_expert_glu_backward": (ctypes.c_int, [P, L, O] + [V] * 10),
         "moe_expert_linear_backward": (ctypes.c_int, [P, L, O] + [V] * 10),
+        "moe_check_router": (ctypes.c_int, [P, R]),
+        "moe_route": (ctypes.c_int, [P, R] + [V] * 6),
+        "moe_route_backward": (ctypes.c_int, [P, R] + [V] * 6),
+        "moe_quantize_mxfp4": (ctypes.c_int, [ctypes.c_int64, ctypes.c_int32] + [V] * 4),
+        "moe_check_expert_mx_op": (ctypes.c_int, [P, O]),
+        "moe_expert_glu_mx": (ctypes.c_int, [P, L, O] + [V] * 8),
+        "moe_expert_linear_mx": (ctypes.c_int, [P, L, O] + [V] * 8),
         "moe_strerror": (ctypes.c_char_p, [ctypes.c_int]),
     }
     for name, (res, args) in sig.items():
@@ -435,11 +452,13 @@ def moe_combine(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor,
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _own_stream(stream, plan: PlanBuffers, *tensors) -> int:
+def _own_stream(stream, plan: PlanBuffers | None, *tensors) -> int:
     """The raw stream to launch on; the kernels run on the current device, so every
     buffer must live there."""
     here = _current_device()
-    for t in (plan.slot, plan.expert_counts, plan.expert_offsets, *tensors):
+    if plan is not None:
+        tensors += (plan.slot, plan.expert_counts, plan.expert_offsets)
+    for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
     if stream is not None:
@@ -571,6 +590,114 @@ def moe_expert_linear_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dy: 
     dw and dbias need a workspace (alloc_expert_workspace)."""
     _expert_backward("moe_expert_linear_backward", lib.moe_expert_linear_backward, 1, p, plan, op, dy,
                      preact, x, w, dz, dx, dw, dbias, workspace, stream)
+
+
+# ---- MX-FP4: quantisation, and the experts' products with MX-FP4 weights -----------
+
+def moe_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
+    """bf16 [..., C] -> MX-FP4 codes uint8 [..., C/2] and scale bytes [..., C/32]."""
+    if x.dim() == 0:
+        raise ValueError("x needs a last dimension of whole 32-value blocks")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    args = (_dev(x, "x", _BF16), _dev(codes, "codes", (torch.uint8,), rows * (cols // 2)),
+            _dev(scales, "scales", (torch.uint8,), rows * (cols // 32)))
+    raw = _own_stream(stream, None, x, codes, scales)
+    _checked(lib.moe_quantize_mxfp4(rows, cols, *args, raw), "moe_quantize_mxfp4")
+
+
+def moe_check_expert_mx_op(p: Problem, op: ExpertOp) -> int:
+    """op.fmt is the rows' format: "mxfp4" or "fp8"."""
+    return int(lib.moe_check_expert_mx_op(ctypes.byref(p), ctypes.byref(op)))
+
+
+def _mx_args(p, plan, op, wide, x, x_scales, w, w_scales, bias):
+    rows, e, k, n = _sizes(p)[0], p.n_experts, op.in_dim, wide * op.out_dim
+    if op.fmt == FMT["fp8"]:
+        args = [_dev(x, "x", (torch.uint8, torch.float8_e4m3fn), rows * k),
+                _dev(x_scales, "x_scales", (torch.float32,), rows * (k // 128))]
+    else:
+        args = [_dev(x, "x", (torch.uint8,), rows * (k // 2)),
+                _dev(x_scales, "x_scales", (torch.uint8,), rows * (k // 32))]
+    _plan_rows(plan, e)
+    return args + [_dev(w, "w", (torch.uint8,), e * n * (k // 2)),
+                   _dev(w_scales, "w_scales", (torch.uint8,), e * n * (k // 32)),
+                   _dev(bias, "bias", (torch.float32,), e * n) or None]
+
+
+def moe_expert_glu_mx(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor, x_scales: torch.Tensor,
+                      w: torch.Tensor, w_scales: torch.Tensor, h: torch.Tensor,
+                      h_scales: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                      stream=None) -> None:
+    """moe_expert_glu with MX-FP4 weights (w uint8 [E, 2F, K/2], w_scales [E, 2F, K/32]) and
+    rows of op.fmt; h bf16 [R_max, F], or with h_scales MX-FP4 codes [R_max, F/2]."""
+    args = _mx_args(p, plan, op, 2, x, x_scales, w, w_scales, bias)
+    rows, n = _sizes(p)[0], op.out_dim
+    if h_scales is None:
+        out = [_dev(h, "h", _BF16, rows * n), None]
+    else:
+        out = [_dev(h, "h", (torch.uint8,), rows * (n // 2)),
+               _dev(h_scales, "h_scales", (torch.uint8,), rows * (n // 32))]
+    raw = _own_stream(stream, plan, x, x_scales, w, w_scales, bias, h, h_scales)
+    _checked(lib.moe_expert_glu_mx(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args,
+                                   *out, raw), "moe_expert_glu_mx")
+
+
+def moe_expert_linear_mx(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor,
+                         x_scales: torch.Tensor, w: torch.Tensor, w_scales: torch.Tensor, y: torch.Tensor,
+                         bias: torch.Tensor | None = None, residual: torch.Tensor | None = None,
+                         stream=None) -> None:
+    """moe_expert_linear with MX-FP4 weights (w uint8 [E, F, K/2], w_scales [E, F, K/32]) and
+    rows of op.fmt; y and residual bf16 [R_max, F]."""
+    args = _mx_args(p, plan, op, 1, x, x_scales, w, w_scales, bias)
+    n = _sizes(p)[0] * op.out_dim
+    args += [_dev(residual, "residual", _BF16, n) or None, _dev(y, "y", _BF16, n)]
+    raw = _own_stream(stream, plan, x, x_scales, w, w_scales, bias, residual, y)
+    _checked(lib.moe_expert_linear_mx(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op),
+                                      *args, raw), "moe_expert_linear_mx")
+
+
+# ---- routing: scores, top-k experts, gate weights ----------------------------------
+
+def router(score: str = "softmax", logits: str = "fp32", n_groups: int = 1, top_groups: int = 1,
+           group_top: int = 1, renormalize: bool = True, scale: float = 1.0) -> Router:
+    """Build a moe_router (logits: the type of logits and dlogits)."""
+    return Router(SCORE[score], LOGITS[logits], n_groups, top_groups, group_top, int(renormalize), scale)
+
+
+def moe_check_router(p: Problem, r: Router) -> int:
+    return int(lib.moe_check_router(ctypes.byref(p), ctypes.byref(r)))
+
+
+def _logits(r: Router):
+    return (torch.float32,) if r.logits == LOGITS["fp32"] else _BF16
+
+
+def moe_route(p: Problem, r: Router, logits: torch.Tensor, topk_ids: torch.Tensor,
+              topk_weights: torch.Tensor | None, bias: torch.Tensor | None = None,
+              scores: torch.Tensor | None = None, stream=None) -> None:
+    """Top-k experts of every token (topk_ids int32 [N, k], -1 where none is left) and their gate
+    weights (float [N, k], or None) from logits [N, E]; scores: float [N, E] or None."""
+    nk, ne = p.n_tokens * p.top_k, p.n_tokens * p.n_experts
+    args = (_dev(logits, "logits", _logits(r), ne), _dev(bias, "bias", (torch.float32,), p.n_experts) or None,
+            _dev(topk_ids, "topk_ids", (torch.int32,), nk),
+            _dev(topk_weights, "topk_weights", (torch.float32,), nk) or None,
+            _dev(scores, "scores", (torch.float32,), ne) or None)
+    raw = _own_stream(stream, None, logits, bias, topk_ids, topk_weights, scores)
+    _checked(lib.moe_route(ctypes.byref(p), ctypes.byref(r), *args, raw), "moe_route")
+
+
+def moe_route_backward(p: Problem, r: Router, logits: torch.Tensor, topk_ids: torch.Tensor | None,
+                       dlogits: torch.Tensor, dweights: torch.Tensor | None = None,
+                       dscores: torch.Tensor | None = None, stream=None) -> None:
+    """dlogits [N, E] from the gradients of moe_route's weights [N, k] and scores [N, E]."""
+    nk, ne = p.n_tokens * p.top_k, p.n_tokens * p.n_experts
+    args = (_dev(logits, "logits", _logits(r), ne), _dev(topk_ids, "topk_ids", (torch.int32,), nk) or None,
+            _dev(dweights, "dweights", (torch.float32,), nk) or None,
+            _dev(dscores, "dscores", (torch.float32,), ne) or None,
+            _dev(dlogits, "dlogits", _logits(r), ne))
+    raw = _own_stream(stream, None, logits, topk_ids, dlogits, dweights, dscores)
+    _checked(lib.moe_route_backward(ctypes.byref(p), ctypes.byref(r), *args, raw), "moe_route_backward")
 
 
 # ---- exchange across EP simulated ranks ---------------------------------------

@@ -5,8 +5,9 @@
  * The library turns top-k expert IDs into a routing plan, packs token rows
  * into an expert-major buffer (optionally quantised to blockwise FP8,
  * MX-FP4 or NVFP4 on the way) and combines expert outputs back into token
- * order, weighted by the gate values.  It also runs the experts' products on
- * the packed rows, and the backward passes of products and combine.  Expert-parallel destination ranks
+ * order, weighted by the gate values.  It also chooses the experts (routing), quantises to
+ * MX-FP4, runs the experts' products on the packed rows, and the backward passes of
+ * routing, products and combine.  Expert-parallel destination ranks
  * are simulated as contiguous segments of the one packed buffer, or, with
  * the moe_exchange_* calls, as separate receive buffers of several
  * simulated source ranks.
@@ -358,6 +359,74 @@ MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
                                  const uint16_t *dout, uint16_t *dy, float *dweights,
                                  void *stream);
 
+/* ---- routing: scores, top-k experts, gate weights ----------------------------
+ *
+ * What stands before moe_dispatch_plan: from a router's logits [N][E] to the IDs and
+ * gate weights that plan, dispatch and combine take.  Per token, with l its logits:
+ *
+ *   scores   s = softmax(l) or sigmoid(l)
+ *   keys     s_e + bias_e in 64 bits; without a bias l_e itself (scores have its order)
+ *   groups   the E experts in n_groups runs of E / n_groups; a group's score is the sum
+ *            of its group_top best s_e + bias_e (in 64 bits; of one: its best key); only
+ *            the top_groups best groups' experts can be chosen
+ *   ids      the k best keys, best first
+ *   weights  scale * s_id, or with renormalize scale * s_id / (sum of the chosen s)
+ *
+ * Ties go to the lower index, of experts and of groups; the order never hangs on an fp32
+ * rounding.  An expert whose logit or key is -inf is never chosen (a switched-off
+ * expert, a row without a token): where fewer than k are left, the other IDs are -1 with
+ * weight 0, which the plan takes as masked.  A row of -inf has scores 0 under softmax.  A NaN
+ * key ranks first, and a NaN logit makes its token's softmax scores NaN: it shows in that
+ * token's weights and in no other's.  Renormalised softmax weights are the softmax
+ * over the chosen logits alone; chosen sigmoid scores that sum to 0 in fp32
+ * (logits below -87) give weights 0.
+ *
+ * p names N, E and k; its other fields are not used here. */
+typedef enum moe_score {
+  MOE_SCORE_SOFTMAX = 0,
+  MOE_SCORE_SIGMOID = 1
+} moe_score;
+typedef enum moe_logits {
+  MOE_LOGITS_F32 = 0,
+  MOE_LOGITS_BF16 = 1
+} moe_logits;
+
+typedef struct moe_router { /* host memory */
+  int32_t score;       /* a moe_score value                                    */
+  int32_t logits;      /* a moe_logits value: type of logits and dlogits       */
+  int32_t n_groups;    /* G >= 1, E % G == 0; 1: no groups                     */
+  int32_t top_groups;  /* 1 .. G, k <= top_groups * (E / G)                    */
+  int32_t group_top;   /* 1 or 2                                               */
+  int32_t renormalize; /* 0 or 1                                               */
+  float scale;         /* finite                                               */
+} moe_router;
+
+/* MOE_OK if r is well formed for p, else the code the calls below return. */
+MOE_API int moe_check_router(const moe_problem *p, const moe_router *r);
+
+/* logits: device [N][E] of r->logits' type; bias: device float [E] or NULL;
+ * topk_ids: int32 [N][k]; topk_weights: float [N][k] or NULL (not computed);
+ * scores: float [N][E] for s (a balance loss reads it), or NULL.  One launch. */
+MOE_API int moe_route(const moe_problem *p, const moe_router *r, const void *logits,
+                      const float *bias, int32_t *topk_ids, float *topk_weights, float *scores,
+                      void *stream);
+
+/* Gradient of moe_route for a training step, from dweights = d loss / d topk_weights
+ * (float [N][k]) and dscores = d loss / d scores (float [N][E]), either of which may be
+ * NULL (zero), not both.  topk_ids: the IDs that were chosen (they are constants; an ID
+ * outside [0, E) is masked and its dweights is not read; one that repeats counts each
+ * time).  With C the chosen pairs, w' = weights / scale:
+ *   renormalize:  u_j = scale * w'_j * (dweights_j - sum_i dweights_i w'_i)
+ *                 dlogits_e = sum_{id_j = e} u_j * f_e + J(dscores)_e
+ *                 f = 1 (softmax), 1 - s_e (sigmoid)
+ *   otherwise     dlogits = J(dscores + sum_{id_j = e} scale * dweights_j)
+ *   J(d)_e = s_e (d_e - sum_f d_f s_f) (softmax), d_e s_e (1 - s_e) (sigmoid)
+ * in fp32, rounded once to dlogits [N][E] (r->logits' type), which is written whole.
+ * The bias has no gradient: it only orders. */
+MOE_API int moe_route_backward(const moe_problem *p, const moe_router *r, const void *logits,
+                               const int32_t *topk_ids, const float *dweights,
+                               const float *dscores, void *dlogits, void *stream);
+
 /* ---- the experts' products over the packed rows ------------------------------
  *
  * Between dispatch and combine: every expert's matrix product over its rows of
@@ -472,6 +541,49 @@ MOE_API int moe_expert_linear_backward(const moe_problem *p, const moe_plan *pla
                                        const uint16_t *w, uint16_t *dz, uint16_t *dx,
                                        uint16_t *dw, float *dbias, void *workspace,
                                        void *stream);
+
+/* ---- MX-FP4: quantisation, and the experts' products with MX-FP4 weights --------
+ *
+ * The weights of the calls below are MX-FP4: codes [E][rows][K/2] and scale bytes
+ * [E][rows][K/32], as moe_quantize_mxfp4 makes them from bf16 [E * rows][K].  x is
+ * MX-FP4 (moe_dispatch's payload and scales) or FP8 (MOE_FMT_FP8_E4M3_B128).
+ *
+ * Encoding is moe_dispatch's (see MOE_FMT_MXFP4_B32), but for a block that holds an
+ * infinity or a NaN: it gets the scale byte 255, E8M0's NaN, and zero codes, so that what
+ * is computed from it is NaN and not a finite guess. */
+
+/* x: device bf16 bits [rows][cols], cols % 32 == 0; codes: uint8 [rows][cols/2];
+ * scales: uint8 [rows][cols/32].  rows >= 0, rows * cols < 2^46. */
+MOE_API int moe_quantize_mxfp4(int64_t rows, int32_t cols, const uint16_t *x, uint8_t *codes,
+                               uint8_t *scales, void *stream);
+
+/* MOE_OK if op is well formed for the calls below: as moe_check_expert_op, with fmt the
+ * rows' format: MOE_FMT_MXFP4_B32 (K a multiple of 32) or MOE_FMT_FP8_E4M3_B128 (of 128),
+ * and F a multiple of 8. */
+MOE_API int moe_check_expert_mx_op(const moe_problem *p, const moe_expert_op *op);
+
+/* moe_expert_glu with MX-FP4 weights [E][2F][K/2], gate rows first.  h: bf16 bits
+ * [R_max][F] with h_scales NULL; else MX-FP4 codes uint8 [R_max][F/2] (F a multiple of 32)
+ * with their scales [R_max][F/32], quantised from the unrounded values: the x of the
+ * next product.  x_scales: uint8 [R_max][K/32] or, for FP8 rows, float [R_max][K/128].
+ * x_scales and w_scales are 4-byte aligned, and readable to the end of the 4-byte
+ * word that holds their last byte (K % 128 != 0: scale rows are no whole words).
+ *
+ * MX-FP4 rows: the scaled matrix instruction multiplies and adds in fp32 (a product is kept to
+ * 2^-21 of the largest term that it is added with).  FP8 rows: within a 128-value block the
+ * products lose the bits that moe_expert_glu's do, cut relative to w's scaled codes;
+ * the blocks' sums are multiplied by x's fp32 scale and added in fp32.  Row
+ * ranges, untouched rows, repeatability and NaN: as the experts' products above. */
+MOE_API int moe_expert_glu_mx(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                              const void *x, const void *x_scales, const uint8_t *w,
+                              const uint8_t *w_scales, const float *bias, void *h,
+                              uint8_t *h_scales, void *stream);
+
+/* moe_expert_linear with MX-FP4 weights [E][F][K/2]; y and residual bf16. */
+MOE_API int moe_expert_linear_mx(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
+                                 const void *x, const void *x_scales, const uint8_t *w,
+                                 const uint8_t *w_scales, const float *bias,
+                                 const uint16_t *residual, uint16_t *y, void *stream);
 
 /* ---- exchange across EP simulated ranks ----------------------------------
  *
