@@ -46,6 +46,21 @@ __device__ __forceinline__ float activate(int act, float z) {
   }
 }
 
+// As with_blocks; a tile of six blocks a wave goes by single ones.
+template <class S, class F>
+__device__ __forceinline__ void with_own_blocks(int rows, F f) {
+  if constexpr (S::FI == 6) {
+    const int blocks = (rows + 16 * S::WI - 1) / (16 * S::WI);
+    if (blocks <= 2) return f(std::integral_constant<int, 2>());
+    if (blocks == 3) return f(std::integral_constant<int, 3>());
+    if (blocks == 4) return f(std::integral_constant<int, 4>());
+    if (blocks == 5) return f(std::integral_constant<int, 5>());
+    return f(std::integral_constant<int, 6>());
+  } else {
+    with_blocks<S>(rows, f);
+  }
+}
+
 template <class S, bool GLU>
 __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kernel(MxArgs g) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
@@ -77,13 +92,15 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
     s.j = {g.w + wrow0 * w_bytes, (wrows - j0) * w_bytes, 0};
     s.x = {g.x_scales + row0 * x_scale_bytes, left * x_scale_bytes};
     s.w = {g.w_scales + wrow0 * blocks, (wrows - j0) * blocks};
-    s.steps = (w_bytes + kStepBytes * S::WK - 1) / (kStepBytes * S::WK);
+    // of a group
+    s.steps = (w_bytes + kStepBytes * S::kSpan * S::WK - 1) / (kStepBytes * S::kSpan * S::WK) * S::kSpan;
+    if constexpr (S::WK == 1) s.steps = (w_bytes + kStepBytes - 1) / kStepBytes;
     return s;
   };
 
   MxSource cur = source(t), following;
-  start<S>(lds, feed, cur);
-  Progress at;
+  MxProgress at;
+  start_mx<S>(lds, feed, cur, at);
   auto one_tile = [&](auto own_blocks) {
     constexpr int FI = decltype(own_blocks)::value;
     constexpr int kTurnCols = GLU ? kWaveCols : S::kTurnCols, kTurns = kWaveCols / kTurnCols;
@@ -93,7 +110,7 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
     const int lane = late_lane_id();
     if constexpr (S::WK > 1) {
       // the groups' sums, added in order by the first, through what is its way out
-      lds_ptr sums = lds + S::NST * S::kStage + lane * 16;
+      lds_ptr sums = lds + S::kLoadLds + lane * 16;
       if (group_id<S>() > 0) {
 #pragma unroll
         for (int b = 0; b < S::FJ; ++b) *(MOE_LDS f32x4 *)(sums + b * kWave * 16) = acc[0][b];
@@ -109,7 +126,7 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
         for (int b = 0; b < S::FJ; ++b)
           acc[0][b] += *(MOE_LDS const f32x4 *)(sums + q * S::kGroupLds + b * kWave * 16);
     }
-    const auto turn = Transpose<kTurnCols>::template make<S>(lds, lane);
+    const Transpose<kTurnCols> turn{lds + S::kLoadLds + group_wave<S>() * Transpose<kTurnCols>::kBytes, lane};
     const float *bias = g.bias ? g.bias + static_cast<int64_t>(t.e) * wrows : nullptr;
     const int col0 = t.j * kCols + w.wj * kWaveCols;  // of the wave
     const int left = t.count - t.i0;                  // rows of the tile
@@ -201,7 +218,7 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
   for (int n = 1; t.e >= 0; ++n) {
     const RowTile next = order.find(n);
     following = source(next);
-    with_blocks<S>(t.count - t.i0, one_tile);
+    with_own_blocks<S>(t.count - t.i0, one_tile);
     t = next;
     cur = following;
   }
@@ -220,8 +237,25 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 
 template <bool GLU, bool FP8, bool ODD>
 hipError_t launch_sized(const MxArgs &g, int64_t pairs, hipStream_t stream) {
+  typedef MxShape<16, 64, 1, 1, FP8 ? 2 : 3, FP8, ODD, 4> Split;
+  typedef MxShape<16, 64, 1, 1, 4, FP8, ODD> Few;
+  typedef MxShape<64, 128, 2, 2, 3, FP8, ODD> Low;
   typedef MxShape<128, 128, 2, 2, 2, FP8, ODD> Some;
-  return launch<Some, GLU>(g, pairs, stream);
+  typedef typename std::conditional<FP8, MxShape<128, 256, 2, 4, 2, FP8, ODD>,
+                                    MxShape<256, 256, 2, 4, 2, FP8, ODD>>::type Many;
+  typedef MxShape<FP8 ? 128 : 384, FP8 ? 256 : 128, FP8 ? 2 : 4, FP8 ? 4 : 2, 2, FP8, ODD> Tall;
+  const int64_t used = pairs < g.n_experts ? pairs : g.n_experts, rows = (pairs + used - 1) / used;
+  const int wrows = g.n * (GLU ? 2 : 1);
+  const int64_t tiles = row_tile_bound<Some::BI>(pairs, g.n_experts) * col_tiles<Some::BJ>(wrows);
+  const int64_t split_tiles = row_tile_bound<Split::BI>(pairs, g.n_experts) * col_tiles<Split::BJ>(wrows);
+  if (g.k >= 2048 && (rows <= 12 || split_tiles <= 2 * kComputeUnits)) return launch<Split, GLU>(g, pairs, stream);
+  if (rows <= 16 && tiles < 4 * kComputeUnits) return launch<Few, GLU>(g, pairs, stream);
+  if (tiles < kEnoughTiles) return launch<Low, GLU>(g, pairs, stream);
+  if (rows <= 112) return launch<Some, GLU>(g, pairs, stream);
+  if (!FP8 && rows < 336) return launch<Tall, GLU>(g, pairs, stream);
+  if (row_tile_bound<Many::BI>(pairs, g.n_experts) * col_tiles<Many::BJ>(wrows) < kEnoughTiles)
+    return launch<Some, GLU>(g, pairs, stream);
+  return launch<Many, GLU>(g, pairs, stream);
 }
 
 template <bool GLU>

@@ -135,7 +135,7 @@ __device__ __forceinline__ i32x4 resource(const void *base, uint32_t bytes) {
   "s_nop 4\n\ts_mov_b32 m0, %[to]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o0], %[r], 0 offen lds\n\t"
 template <int STRIDE, int L>
 __device__ __forceinline__ void load_lds16(i32x4 r, lds_ptr to, const uint32_t (&o)[L]) {
-  static_assert(L == 1 || L == 2 || L == 4 || L == 8, "whole groups");
+  static_assert(L == 1 || L == 2 || L == 4 || L == 6 || L == 8, "whole groups");
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<size_t>(to)));
   if constexpr (L == 1)
     asm volatile(MOE_TO_LDS_FIRST ::[o0] "v"(o[0]), [r] "s"(r), [to] "s"(at) : "memory", "m0", "scc");
@@ -146,6 +146,11 @@ __device__ __forceinline__ void load_lds16(i32x4 r, lds_ptr to, const uint32_t (
   if constexpr (L == 4)
     asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3)::[o0] "v"(o[0]), [o1] "v"(o[1]),
                  [o2] "v"(o[2]), [o3] "v"(o[3]), [r] "s"(r), [to] "s"(at), [stride] "n"(STRIDE)
+                 : "memory", "m0", "scc");
+  if constexpr (L == 6)
+    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3) MOE_TO_LDS(4) MOE_TO_LDS(5)::[o0] "v"(o[0]),
+                 [o1] "v"(o[1]), [o2] "v"(o[2]), [o3] "v"(o[3]), [o4] "v"(o[4]), [o5] "v"(o[5]), [r] "s"(r),
+                 [to] "s"(at), [stride] "n"(STRIDE)
                  : "memory", "m0", "scc");
   if constexpr (L == 8)
     asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3) MOE_TO_LDS(4) MOE_TO_LDS(5)

@@ -13,13 +13,20 @@
 //     that both their scale bytes come in one 16-bit read.  The instruction scales and adds to
 //     the fp32 accumulator: nothing is left for the vector units.
 //   FP8 rows: a half is a 128-value block of the rows, whose products go to a sum of their own
-//     (the weights' scales applied); times the row's fp32 scale it is added up.
+//     (the weights' scales applied); times the row's fp32 scale it is added up.  The
+//     instruction aligns the products of eight neighbouring values to the largest of them and cuts
+//     each to a multiple of 2^(E-13), E the largest sum of the two codes' exponents.  So the
+//     codes of 2 and above (2^1 .. 2^8 with 3 bits below) go through one instruction and those
+//     below 2 (2^-9 .. 1.875) through another: with the weights' codes (1/2 .. 6) every product is
+//     a multiple of 2^(E-13), and nothing is cut.
 //
-// Scales go to LDS like the operands, a step's 8 bytes of a row as two 4-byte words (two
-// blocks' fp32 scales of an FP8 row are as many).  Where scale rows are no whole words (K % 128
-// != 0: ODD) it is the three words that the 8 bytes touch.  A scale byte past its row's
-// end must not be the next row's NaN: words past it are not loaded (zero: 2^-127, times
-// zero codes), bytes of a word past it are cleared after the read.
+// Scales go to LDS like the operands, but 16 bytes of a row at a time: every lane of such a load
+// touches a line of its own, and it is these requests, not the bytes, that cost (a 4-byte word a
+// lane each step: as many requests as the operands' own, and 1790 us for 1285 without
+// them; 256 experts of 256 rows, K = 7168, F = 2048).  A piece is two steps of a row (of an
+// FP8 row: four blocks' fp32 scales).  Where scale rows are no whole words (K % 128 != 0: ODD)
+// a piece is the words that one step's 8 bytes touch.  A scale past its row's end must not be the
+// next row's, which may be NaN: it is cleared after the read (2^-127, times zero codes).
 #pragma once
 
 #include "expert_tile.hpp"
@@ -39,19 +46,24 @@ struct MxShape {
   static constexpr int kLoadRows = kThreads / 8;
   static constexpr int kBytesPart = LI * kThreads * 16;  // of I: 128 bytes of each row
   static constexpr int kBytesI = kParts * kBytesPart, kBytesJ = LJ * kThreads * 16;
-  static constexpr int kWords = ODD ? 3 : 2;  // of scales, a row and step
-  static constexpr int scale_loads(int b) { return (b * kWords + kThreads - 1) / kThreads; }
-  static constexpr int LSI = scale_loads(BI), LSJ = scale_loads(BJ);
-  static constexpr int kBytesSI = LSI * kThreads * 4, kBytesSJ = LSJ * kThreads * 4;
-  static constexpr int kStage = kBytesI + kBytesJ + kBytesSI + kBytesSJ;
+  // pieces of scales: 64 rows a load, of I, then of J, dealt to the waves
+  static constexpr int kWaves = WI * WJ, kGroupsI = (BI + 63) / 64, kGroups = kGroupsI + (BJ + 63) / 64;
+  static constexpr int kSpan = ODD ? 1 : 2;           // steps of a piece
+  // that NST steps in a row can lie in: a tile's last step may have one to itself
+  static constexpr int kPieces = ODD ? NST : NST / 2 + 1 + NST % 2;
+  static constexpr int kPieceBytes = kGroups * 1024;
+  static constexpr int kStage = kBytesI + kBytesJ;
+  static constexpr int kLoadLds = NST * kStage + kPieces * kPieceBytes;
   static constexpr int kWaveCols = BJ / WJ;
   static constexpr int kTurnCols = WK == 1 && kWaveCols > 32 ? 32 : kWaveCols;
-  static constexpr int kGroupLds = NST * kStage + WI * WJ * 16 * kTurnCols * 4;
+  static constexpr int kGroupLds = kLoadLds + WI * WJ * 16 * kTurnCols * 4;
   static constexpr int kLdsBytes = WK * kGroupLds;
   static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (WI * WJ * WK);
   static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
   static constexpr int kWavesPerSimd = kResident * WI * WJ * WK >= 8 ? 2 : 1;
-  static constexpr int kLoads = kParts * LI + LJ + LSI + LSJ;
+  // loads of a wave and stage, without the pieces of scales (which a wave may have or not: what
+  // waits for a stage then waits for those behind it too)
+  static constexpr int kLoads = kParts * LI + LJ;
   static_assert(!(FP8 && ODD), "FP8 rows have whole 128-value blocks");
   static_assert(BI % (16 * WI) == 0 && BJ % (16 * WJ) == 0, "whole blocks");
   static_assert(kLoads * (NST - 1) < 64, "the wait counter holds 63 loads");
@@ -65,27 +77,21 @@ struct ScaleRows {
   int bytes;
 };
 
-// A launch's lanes for the scales of B tile rows; ROW as in Along.
-template <class S, int B, int N, class ROW>
-struct WordLanes {
+// A launch's lanes for the scales: 64 tile rows, from row `first` on; ROW as in Along.
+template <class S, class ROW>
+struct PieceLanes {
   ROW row;
   int row_bytes;
   __device__ __forceinline__ void init(int bytes) { row_bytes = bytes; }
-  __device__ __forceinline__ void issue(lds_ptr to, const ScaleRows &s, int step) const {
-    const int tid = group_thread<S>(), at = step * 8;
-    to += group_wave<S>() * kWave * 4;
+  // the 16 bytes from byte `at` of each row on
+  __device__ __forceinline__ void issue(lds_ptr to, const ScaleRows &s, int first, int rows, int at) const {
     // whole words from the one on that holds the first byte
     const int skip = S::ODD ? static_cast<int>(reinterpret_cast<uintptr_t>(s.base) & 3) : 0;
     const auto r = resource(s.base - skip + at, s.bytes == 0 ? 0 : max(((s.bytes + skip + 3) & ~3) - at, 0));
-#pragma unroll
-    for (int u = 0; u < N; ++u) {
-      const int i = u * S::kThreads + tid;
-      const int d = S::ODD ? i % 3 : i / B, tr = S::ODD ? i / 3 : i % B;
-      const int start = static_cast<int>(row(tr)) * row_bytes + skip;
-      const int word = (S::ODD ? start & ~3 : start) + d * 4;
-      const bool in = (S::ODD ? tr < B : d < 2) && word + at < start + row_bytes;
-      load_lds4(r, to + u * S::kThreads * 4, in ? static_cast<uint32_t>(word) : kNowhere);
-    }
+    const int tr = first + lane_id(), start = static_cast<int>(row(tr)) * row_bytes + skip;
+    const int word = S::ODD ? start & ~3 : start;
+    const uint32_t place[1] = {tr < rows && word + at < start + row_bytes ? static_cast<uint32_t>(word) : kNowhere};
+    load_lds16<0>(r, to, place);
   }
 };
 
@@ -104,29 +110,66 @@ __device__ __forceinline__ MxSource either(bool c, const MxSource &a, const MxSo
   return s;
 }
 
+// Where a workgroup stands in the ring of pieces.
+struct Ring {
+  int at = 0;
+  template <int N>
+  __device__ __forceinline__ void advance() {
+    at = at + 1 == N ? 0 : at + 1;
+  }
+};
+
 template <class S, class ROW>
 struct MxFeed {
   Along<S, S::LI, SameRow> i;
   Along<S, S::LJ, ROW> j;
-  WordLanes<S, S::BI, S::LSI, SameRow> x;
-  WordLanes<S, S::BJ, S::LSJ, ROW> w;
-  __device__ __forceinline__ void issue(lds_ptr lds, int stage, const MxSource &src, int step) const {
-    lds_ptr to = lds + stage * S::kStage;
-    if constexpr (S::WK > 1) step = step * S::WK + group_id<S>();
+  PieceLanes<S, SameRow> x;
+  PieceLanes<S, ROW> w;
+  // step of the contraction that a group takes as its step-th
+  __device__ __forceinline__ int global_step(int step) const {
+    if constexpr (S::WK == 1) return step;
+    if constexpr (S::ODD) return step * S::WK + group_id<S>();
+    return (step / 2 * S::WK + group_id<S>()) * 2 + step % 2;  // (pieces stay whole)
+  }
+  __device__ __forceinline__ void issue(lds_ptr lds, int stage, Ring &piece, const MxSource &src, int step) const {
+    const int t = global_step(step);
+    if (step % S::kSpan == 0) {
+      lds_ptr to = lds + S::NST * S::kStage + piece.at * S::kPieceBytes;
+      piece.template advance<S::kPieces>();
 #pragma unroll
-    for (int p = 0; p < S::kParts; ++p) i.issue(to + p * S::kBytesPart, src.i, step * S::kParts + p);
-    j.issue(to + S::kBytesI, src.j, step);
-    x.issue(to + S::kBytesI + S::kBytesJ, src.x, step);
-    w.issue(to + S::kBytesI + S::kBytesJ + S::kBytesSI, src.w, step);
+      for (int u = 0; u < (S::kGroups + S::kWaves - 1) / S::kWaves; ++u) {
+        const int g = u * S::kWaves + group_wave<S>();
+        if (g < S::kGroupsI)
+          x.issue(to + g * 1024, src.x, g * 64, S::BI, t * 8);
+        else if (g < S::kGroups)
+          w.issue(to + g * 1024, src.w, (g - S::kGroupsI) * 64, S::BJ, t * 8);
+      }
+    }
+    lds_ptr to = lds + stage * S::kStage;
+#pragma unroll
+    for (int p = 0; p < S::kParts; ++p) i.issue(to + p * S::kBytesPart, src.i, t * S::kParts + p);
+    j.issue(to + S::kBytesI, src.j, t);
   }
 };
+
+// Where a workgroup stands between tiles.
+struct MxProgress : Progress {
+  Ring loaded, read;  // the piece that is loaded next; that of the next tile's first step
+};
+
+// The loads of the first tile's first NST steps.
+template <class S, class F>
+__device__ __forceinline__ void start_mx(lds_ptr lds, const F &feed, const MxSource &src, MxProgress &at) {
+#pragma unroll
+  for (int s = 0; s < S::NST; ++s) feed.issue(lds, s, at.loaded, src, s);
+}
 
 // acc[a][b] = the products of cur's steps; as multiply() of expert_tile.hpp.
 // skip_i, skip_j (ODD): what ScaleRows' first byte is past a whole word; blocks: scale blocks
 // of a row.
 template <class S, int FI, class F>
 __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const MxSource &cur,
-                                            const MxSource &next, int blocks, Progress &at,
+                                            const MxSource &next, int blocks, MxProgress &at,
                                             f32x4 (&acc)[FI][S::FJ]) {
   const Wave<S> w = this_wave<S>();
   const int lane = lane_id(), r = lane & 15, q = lane >> 4;
@@ -136,20 +179,17 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
   const int swap = S::FP8 ? 64 : 16;  // between the halves (of an FP8 part: between a lane's chunks)
   const int at_i = row_i * kStepBytes + ((chunk ^ (r & 7)) * 16);
   const int at_j = row_j * kStepBytes + ((chunk ^ (r & 7)) * 16);
-  // and of their scales
-  int scale_i, scale_j;
+  // and, in a piece, of their scales
+  int scale_i = row_i * 16, scale_j = S::kGroupsI * 1024 + row_j * 16;
   if constexpr (S::FP8) {
-    scale_i = row_i * 4;
-    scale_j = row_j * 4 + q;
+    scale_j += q;
   } else if constexpr (S::ODD) {
-    const int skip_i = static_cast<int>(reinterpret_cast<uintptr_t>(cur.x.base) & 3);
-    const int skip_j = static_cast<int>(reinterpret_cast<uintptr_t>(cur.w.base) & 3);
     // (16 rows on, and an even number of gate rows on, a row starts at the same place in a word)
-    scale_i = row_i * 12 + ((r * blocks + skip_i) & 3) + 2 * q;
-    scale_j = row_j * 12 + ((r * blocks + skip_j) & 3) + 2 * q;
+    scale_i += ((r * blocks + static_cast<int>(reinterpret_cast<uintptr_t>(cur.x.base) & 3)) & 3) + 2 * q;
+    scale_j += ((r * blocks + static_cast<int>(reinterpret_cast<uintptr_t>(cur.w.base) & 3)) & 3) + 2 * q;
   } else {
-    scale_i = (q >> 1) * S::BI * 4 + row_i * 4 + (q & 1) * 2;
-    scale_j = (q >> 1) * S::BJ * 4 + row_j * 4 + (q & 1) * 2;
+    scale_i += 2 * q;
+    scale_j += 2 * q;
   }
 #pragma unroll
   for (int a = 0; a < FI; ++a)
@@ -158,56 +198,66 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
 
   const int steps = max(cur.steps, S::NST);
   int stage = at.stage;
+  lds_ptr pieces = lds + S::NST * S::kStage, scales = pieces + at.read.at * S::kPieceBytes;
   auto turn_over = [&](int t) {
     wait_behind<S::kLoads *(S::NST - 2)>(t < S::NST - 1 ? at.younger : 0);
     const int s = t + S::NST;
     const bool mine = s < steps;
-    feed.issue(lds, stage, either(mine, cur, next), mine ? s : s - steps);
+    feed.issue(lds, stage, at.loaded, either(mine, cur, next), mine ? s : s - steps);
     stage = stage + 1 == S::NST ? 0 : stage + 1;
+    if (t + 1 == steps || (t + 1) % S::kSpan == 0) {
+      at.read.template advance<S::kPieces>();
+      scales = pieces + at.read.at * S::kPieceBytes;
+    } else {
+      scales += 8;
+    }
   };
-  wait_behind<S::kLoads *(S::NST - 1)>(at.younger);
+  wait_behind<S::kLoads *(S::NST - 1)>(at.younger);  // (the first step's pieces come before its operands)
 
   i32x8 vi[2];
   i32x4 vj[S::FJ];
   float fi[2];                                      // FP8: the rows' scales
   int si[S::FP8 ? 1 : FI] = {}, sj[S::FJ];          // MX: both halves' bytes; FP8: one half's
-  int mask = 0xFFFF;                                // ODD: of the step that si and sj belong to
+  // scale bytes of the step that si and sj belong to that lie in the row (a piece past the
+  // row's end holds the next row's)
+  int mask[S::FP8 ? 2 : 1];
   typedef uint16_t __attribute__((aligned(1), may_alias)) loose16;
   auto short_at = [&](lds_ptr p) -> int {
     if constexpr (S::ODD)
-      return *(MOE_LDS const loose16 *)p & mask;
+      return *(MOE_LDS const loose16 *)p & mask[0];
     else
-      return *(MOE_LDS const uint16_t *)p;
+      return *(MOE_LDS const uint16_t *)p & mask[0];
   };
-  // scale bytes that lie past the row's end in step t are cleared
   auto set_mask = [&](int t) {
-    if constexpr (S::ODD) {
-      if constexpr (S::WK > 1) t = t * S::WK + group_id<S>();
-      const int left = blocks - t * 8 - 2 * q;
-      mask = left >= 2 ? 0xFFFF : left == 1 ? 0xFF : 0;
+    const int left = blocks - feed.global_step(t) * 8;
+    if constexpr (S::FP8) {
+      mask[0] = left > 0 ? -1 : 0;  // (whole 128-value blocks)
+      mask[1] = left > 4 ? -1 : 0;
+    } else {
+      mask[0] = left - 2 * q >= 2 ? 0xFFFF : left - 2 * q == 1 ? 0xFF : 0;
     }
   };
   auto read_i = [&](int set, int blk, int half) {
-    lds_ptr ti = lds + stage * S::kStage, ts = ti + S::kBytesI + S::kBytesJ;
+    lds_ptr ti = lds + stage * S::kStage;
     const int block = blk * S::WI * 16;
     if constexpr (S::FP8) {
       lds_ptr p = ti + half * S::kBytesPart + block * kStepBytes;
       vi[set] = __builtin_shufflevector(*(MOE_LDS const i32x4 *)(p + at_i), *(MOE_LDS const i32x4 *)(p + (at_i ^ 64)),
                                         0, 1, 2, 3, 4, 5, 6, 7);
-      fi[set] = *(MOE_LDS const float *)(ts + scale_i + half * S::BI * 4 + block * 4);
+      fi[set] = __builtin_bit_cast(float, *(MOE_LDS const int *)(scales + scale_i + half * 4 + block * 16) & mask[half]);
     } else {
       const i32x4 v = *(MOE_LDS const i32x4 *)(ti + (half ? at_i ^ swap : at_i) + block * kStepBytes);
       vi[set] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-      if (half == 0) si[blk] = short_at(ts + scale_i + block * (S::ODD ? 12 : 4));
+      if (half == 0) si[blk] = short_at(scales + scale_i + block * 16);
     }
   };
   auto read_j = [&](int b, int half) {
-    lds_ptr tj = lds + stage * S::kStage + S::kBytesI, ts = tj + S::kBytesJ + S::kBytesSI;
+    lds_ptr tj = lds + stage * S::kStage + S::kBytesI;
     vj[b] = *(MOE_LDS const i32x4 *)(tj + (half ? at_j ^ swap : at_j) + b * 16 * kStepBytes);
     if constexpr (S::FP8)
-      sj[b] = *(MOE_LDS const uint8_t *)(ts + scale_j + half * S::BJ * 4 + b * 16 * 4);
+      sj[b] = *(MOE_LDS const uint8_t *)(scales + scale_j + half * 4 + b * 256) & mask[half];
     else if (half == 0)
-      sj[b] = short_at(ts + scale_j + b * 16 * (S::ODD ? 12 : 4));
+      sj[b] = short_at(scales + scale_j + b * 256);
   };
   auto wide = [](i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); };
 
@@ -227,13 +277,24 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
       }
       read_i(set ^ 1, last ? 0 : a + 1, last ? H ^ 1 : H);
       if constexpr (S::FP8) {
+        // codes of 2 and above have the top bit of their exponent set
+        i32x8 high, low;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t v = static_cast<uint32_t>(vi[set][i]), one = (v >> 6) & 0x01010101u;
+          const uint32_t all = (one << 8) - one;  // 255 in each such byte
+          high[i] = static_cast<int>(v & all);
+          low[i] = static_cast<int>(v & ~all);
+        }
         // the product of block b, then what that of b - 1 adds to its sum
         f32x4 d[2];
 #pragma unroll
         for (int b = 0; b <= S::FJ; ++b) {
           if (b < S::FJ) {
             d[b & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                wide(vj[b]), vi[set], f32x4{0.f, 0.f, 0.f, 0.f}, 4, 0, 0, sj[b], 0, 127);
+                wide(vj[b]), low, f32x4{0.f, 0.f, 0.f, 0.f}, 4, 0, 0, sj[b], 0, 127);
+            d[b & 1] =
+                __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(vj[b]), high, d[b & 1], 4, 0, 0, sj[b], 0, 127);
             if (last) read_j(b, H ^ 1);
           }
           if (b > 0) {

@@ -4,10 +4,13 @@
 //   s = softmax(l) or sigmoid(l);  experts in order of s + bias (of l without a bias);
 //   w_j = scale * s_j, or scale * s_j / sum_i s_i over the chosen ones
 //
-// A token is a run of L lanes of a wave (16 or 64), each with PER neighbouring experts
-// in registers; the k <= L choices end one to a lane.  The order of two experts must
-// not hang on a rounding, so keys are compared as whole numbers: without a bias the logits'
-// own bits, with one the bits of s + bias in 64 bits.
+// A token is a run of L lanes of a wave (16, 32 or 64), each with PER neighbouring experts
+// in registers; the k <= L choices end one to a lane.  Keys are compared as whole numbers in
+// the values' order.  The order of two experts must not hang on a rounding.  Without a bias it is
+// that of the logits, which is exact.  With one, and for sums of two in a group, values are formed
+// in fp32 first; where two that are told apart lie nearer than their errors could
+// move them, the wave forms all of them again in 64 bits (8192 tokens, 256 experts, 8 groups:
+// 64 bits for every token took 29.6 us).
 #include <initializer_list>
 #include <type_traits>
 
@@ -20,34 +23,50 @@ namespace {
 constexpr int kThreads = 256;
 constexpr float kInf = __builtin_inff();
 
-// -------------------------------------------------- a token's lanes ---
-
-template <int L>
-__device__ __forceinline__ uint32_t other(uint32_t v, int step) {
-  return static_cast<uint32_t>(__shfl_xor(static_cast<int>(v), step));
+// a or b, as values: of two array elements `c ? a : b` chooses the place, and what follows
+// from that is an array indexed by a register, resolved with a chain of selects at every use.
+template <class V>
+__device__ __forceinline__ V pick(bool c, V a, V b) {
+  return c ? a : b;
 }
+
+// -------------------------------------------------- a token's lanes ---
 
 // f(v of a lane, v of its partner) over the L lanes of a token, in a fixed order: every
 // lane ends with the same bits.
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+// v of this lane and of the lane STEP away, in either order (f is symmetric).
+template <int STEP>
+__device__ __forceinline__ u32x2 both(uint32_t v) {
+  if constexpr (STEP == 1) return u32x2{v, dpp<kQuadSwap1>(v)};
+  if constexpr (STEP == 2) return u32x2{v, dpp<kQuadSwap2>(v)};
+  if constexpr (STEP == 4) return u32x2{v, dpp<kRowHalfMirror>(v)};
+  if constexpr (STEP == 8) return u32x2{v, dpp<kRowMirror>(v)};
+  // odd rows (the upper half) of the first change places with even rows (the lower half) of the second
+  if constexpr (STEP == 16) return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane16_swap(v, v, false, false));
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_permlane32_swap(v, v, false, false));
+}
+template <int STEP, class V, class F>
+__device__ __forceinline__ V with_partner(V v, F f) {
+  if constexpr (sizeof(V) == 8) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const u32x2 lo = both<STEP>(static_cast<uint32_t>(b)), hi = both<STEP>(static_cast<uint32_t>(b >> 32));
+    return f(__builtin_bit_cast(V, static_cast<uint64_t>(hi.x) << 32 | lo.x),
+             __builtin_bit_cast(V, static_cast<uint64_t>(hi.y) << 32 | lo.y));
+  } else {
+    const u32x2 p = both<STEP>(__builtin_bit_cast(uint32_t, v));
+    const uint32_t x = p.x, y = p.y;  // (a cast of a vector's element takes the first one)
+    return f(__builtin_bit_cast(V, x), __builtin_bit_cast(V, y));
+  }
+}
 template <int L, class V, class F>
 __device__ __forceinline__ V all_lanes(V v, F f) {
-  auto with = [&](auto move) {
-    if constexpr (sizeof(V) == 8) {
-      const uint64_t b = __builtin_bit_cast(uint64_t, v);
-      const uint64_t lo = move(static_cast<uint32_t>(b)), hi = move(static_cast<uint32_t>(b >> 32));
-      v = f(v, __builtin_bit_cast(V, hi << 32 | lo));
-    } else {
-      v = f(v, __builtin_bit_cast(V, move(__builtin_bit_cast(uint32_t, v))));
-    }
-  };
-  with([](uint32_t b) { return dpp<kQuadSwap1>(b); });
-  with([](uint32_t b) { return dpp<kQuadSwap2>(b); });
-  with([](uint32_t b) { return dpp<kRowHalfMirror>(b); });
-  with([](uint32_t b) { return dpp<kRowMirror>(b); });
-  if constexpr (L == 64) {
-    with([](uint32_t b) { return other<L>(b, 16); });
-    with([](uint32_t b) { return other<L>(b, 32); });
-  }
+  v = with_partner<1>(v, f);
+  v = with_partner<2>(v, f);
+  v = with_partner<4>(v, f);
+  v = with_partner<8>(v, f);
+  if constexpr (L >= 32) v = with_partner<16>(v, f);
+  if constexpr (L >= 64) v = with_partner<32>(v, f);
   return v;
 }
 template <int L, class V>
@@ -63,12 +82,31 @@ __device__ __forceinline__ K lanes_best(K v) {
   return all_lanes<L>(v, [](K a, K b) { return a > b ? a : b; });
 }
 
-// Lowest lane of this token for which p holds, counted from its first; -1: none.
-template <int L>
-__device__ __forceinline__ int first_lane(bool p) {
-  uint64_t m = ballot(p);
-  if constexpr (L < kWave) m = (m >> (lane_id() & ~(L - 1))) & ((1ull << L) - 1);
-  return m ? __builtin_ctzll(m) : -1;
+// v of a lane that holds what the lane STEP away does.
+template <int STEP, class V>
+__device__ __forceinline__ V partner(V v) {
+  auto one = [](uint32_t u) {
+    const u32x2 p = both<STEP>(u);
+    const uint32_t x = p.x, y = p.y;
+    return STEP >= 16 && (lane_id() & STEP) ? x : y;
+  };
+  if constexpr (sizeof(V) == 8)
+    return static_cast<V>(one(static_cast<uint32_t>(v >> 32))) << 32 | one(static_cast<uint32_t>(v));
+  else
+    return one(v);
+}
+
+// v of a lane of the token (the same number in every lane).
+template <int L, class V>
+__device__ __forceinline__ V lane_value(V v, int lane) {
+  auto one = [&](uint32_t u) -> uint32_t {
+    if constexpr (L == kWave) return __builtin_amdgcn_readlane(u, lane);
+    return __shfl(static_cast<int>(u), lane, L);
+  };
+  if constexpr (sizeof(V) == 8)
+    return static_cast<V>(one(static_cast<uint32_t>(v >> 32))) << 32 | one(static_cast<uint32_t>(v));
+  else
+    return one(v);
 }
 
 // ---------------------------------------------------------- keys ---
@@ -76,16 +114,14 @@ __device__ __forceinline__ int first_lane(bool p) {
 // Whole numbers in the order of the values: above 0 (not to be chosen) for every value
 // but -inf; both zeros alike; a NaN above all.
 __device__ __forceinline__ uint32_t order_key(float v) {
-  if (v != v) return 0xFFFFFFFFu;
-  if (v == -kInf) return 0;
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+  const uint32_t key = u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+  return pick(v != v, 0xFFFFFFFFu, pick(v == -kInf, 0u, key));
 }
 __device__ __forceinline__ uint64_t order_key(double v) {
-  if (v != v) return ~0ull;
-  if (v == -__builtin_inf()) return 0;
   const uint64_t u = __builtin_bit_cast(uint64_t, v + 0.0);
-  return u ^ (u >> 63 ? ~0ull : 1ull << 63);
+  const uint64_t key = u ^ (static_cast<uint64_t>(static_cast<int64_t>(u) >> 63) | 1ull << 63);
+  return pick(v != v, ~uint64_t{0}, pick(v == -__builtin_inf(), uint64_t{0}, key));
 }
 
 // exp to about one unit in the last place (the hardware's exp2 with the argument's
@@ -185,11 +221,11 @@ __device__ __forceinline__ float load_one(const uint16_t *p) {
   return __uint_as_float(static_cast<uint32_t>(*p) << 16);
 }
 
-// Softmax of a row held PER to a lane: v becomes exp(l - max), the result is their
-// sum's reciprocal (0 for a row of -inf; NaN where a NaN or +inf is in the row).
+// Softmax of a row held PER to a lane: v becomes exp(l - top), top the row's maximum; the result is
+// their sum's reciprocal (0 for a row of -inf; NaN where a NaN or +inf is in the row).
 template <int L, int PER>
-__device__ __forceinline__ float softmax_parts(const float (&l)[PER], float (&v)[PER]) {
-  float top = -kInf;
+__device__ __forceinline__ float softmax_parts(const float (&l)[PER], float (&v)[PER], float &top) {
+  top = -kInf;
 #pragma unroll
   for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
   top = lanes_max<L>(top);
@@ -230,78 +266,217 @@ __device__ __forceinline__ void scores64(const float (&l)[PER], bool sigmoid, do
 
 // ----------------------------------------------------- selection ---
 
-// The k largest keys of a token, best first; lane j gets the expert of the j-th, -1 where
-// none is left.
-template <int L, int PER, class K>
-__device__ __forceinline__ int choose(K (&key)[PER], int k) {
-  const int lane = lane_id() & (L - 1);
-  int mine = -1;
-  for (int j = 0; j < k; ++j) {
-    K best = 0;
-    int at = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const bool more = key[i] > best;
-      best = more ? key[i] : best;
-      at = more ? i : at;
-    }
-    const K top = lanes_best<L>(best);
-    const int who = first_lane<L>(best == top && top != 0);  // the lowest index of the best
-    const int slot = __shfl(at, who < 0 ? 0 : who, L);
-    if (lane == j) mine = who < 0 ? -1 : who * PER + slot;
-    if (lane == who) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (i == slot) key[i] = 0;
-    }
-  }
-  return mine;
+// The value of a key (that of -0 is +0).
+__device__ __forceinline__ float key_value(uint32_t u) {
+  return u == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ double key_value(uint64_t u) {
+  return u == ~0ull ? __builtin_nan("") : __builtin_bit_cast(double, u ^ (u >> 63 ? 1ull << 63 : ~0ull));
 }
 
-// Keys of experts outside the best groups become 0.  value: an expert's part of its
-// group's score, -inf if it cannot be chosen.  `row`: an LDS row of L * PER keys.
-template <int L, int PER, class K>
-__device__ __forceinline__ void keep_groups(const RouteArgs &g, const double (&value)[PER], uint64_t *row,
-                                            K (&key)[PER]) {
-  const int lane = lane_id() & (L - 1), e0 = lane * PER;
-  auto of = [](uint64_t u) {
-    return u == ~0ull ? __builtin_nan("") : __builtin_bit_cast(double, u ^ (u >> 63 ? 1ull << 63 : ~0ull));
-  };
-  __builtin_amdgcn_wave_barrier();
+// Whether fp32 values a >= b could be the other way round, or equal: `slack` is what the errors of
+// two scores (or of two sums of two) can come to, 2^-21 what the additions round.
+// A sigmoid is off by at most 4.2 * 2^-24 (exp_fine's error and that of its argument weigh s (1 - s),
+// the sum and the reciprocal 1.5 * 2^-23 s), four of them by 2^-19.  A softmax score is off by at
+// most 27 * 2^-24 of itself (a sum of 1024 terms, 16 in a lane), and scores of a row add up to 1
+// at most: two sets of them by 2^-18.  (A NaN or two infinities are not near: neither becomes
+// another value in 64 bits.)
+constexpr float kSigmoidSlack = 0x1p-19f, kSoftmaxSlack = 0x1p-18f;
+__device__ __forceinline__ bool too_near(float a, float b, float slack) {
+  return a - b <= slack + 0x1p-21f * fabsf(a);
+}
+
+// The k largest keys of a token, best first; lane j gets the expert of the j-th, -1 where
+// none is left.  near: two neighbours in that order, the first left out among
+// them, are too near to tell (fp32 keys that stand for others).
+//
+// A lane sorts its four keys once (a stable network), and offers its best; of the lanes that
+// have the largest the one with the lowest index gives it up: two reductions a choice, and no
+// more than five registers change.  (More keys a lane: it looks for its best again each time.)
+template <int L, int PER, bool NEAR, class K>
+__device__ __forceinline__ int choose(K (&key)[PER], int k, float slack, bool &near) {
+  const int lane = lane_id() & (L - 1);
+  constexpr bool kSorted = PER <= 4;
+  int slot[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) row[e0 + i] = order_key(value[i]);
-  __builtin_amdgcn_wave_barrier();
-  // a group's key takes the place of its first expert's
-  for (int q = lane; q < g.groups; q += L) {
-    uint64_t first = 0, second = 0;
-    for (int i = 0; i < g.group_size; ++i) {
-      const uint64_t u = row[q * g.group_size + i];
-      if (u > first) {
-        second = first;
-        first = u;
-      } else if (u > second) {
-        second = u;
+  for (int i = 0; i < PER; ++i) slot[i] = lane * PER + i;
+  if constexpr (kSorted) {
+#pragma unroll
+    for (int n = PER - 1; n > 0; --n)
+#pragma unroll
+      for (int i = 0; i < n; ++i) {
+        const bool swap = key[i + 1] > key[i];
+        const K high = pick(swap, key[i + 1], key[i]), low = pick(swap, key[i], key[i + 1]);
+        const int first = pick(swap, slot[i + 1], slot[i]), second = pick(swap, slot[i], slot[i + 1]);
+        key[i] = high;
+        key[i + 1] = low;
+        slot[i] = first;
+        slot[i + 1] = second;
+      }
+  }
+  int mine = -1;
+  K last = 0;
+  for (int j = 0; j < k + (NEAR ? 1 : 0); ++j) {
+    K best = key[0];
+    int at = slot[0];
+    if constexpr (!kSorted) {
+#pragma unroll
+      for (int i = 1; i < PER; ++i) {
+        const bool more = key[i] > best;
+        best = pick(more, key[i], best);
+        at = pick(more, slot[i], at);
       }
     }
-    if (g.group_top == 2 && second != 0) first = order_key(of(first) + of(second));
-    row[q * g.group_size] = first;
+    const K top = lanes_best<L>(best);
+    if constexpr (NEAR) {
+      if (j > 0 && top != 0) near = near || too_near(key_value(last), key_value(top), slack);
+      last = top;
+    }
+    int id;
+    bool gives;  // (with nothing left: a key of 0 becomes 0)
+    if constexpr (L == kWave) {
+      const int who = __builtin_ctzll(ballot(best == top));
+      id = __builtin_amdgcn_readlane(at, who);
+      gives = lane == who;
+    } else {
+      const int offer = best == top ? at : 0x7FFFFFFF;
+      id = all_lanes<L>(offer, [](int a, int b) { return a < b ? a : b; });
+      gives = offer == id;
+    }
+    if (lane == j) mine = top != 0 ? id : -1;
+    if constexpr (kSorted) {
+#pragma unroll
+      for (int i = 0; i + 1 < PER; ++i) {
+        key[i] = pick(gives, key[i + 1], key[i]);
+        slot[i] = pick(gives, slot[i + 1], slot[i]);
+      }
+      key[PER - 1] = pick(gives, K{0}, key[PER - 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = pick(gives && slot[i] == id, K{0}, key[i]);
+    }
   }
-  __builtin_amdgcn_wave_barrier();
+  return lane < k ? mine : -1;
+}
+
+// A group's key from its two best (0: none): the best, or with `two` the sum's.
+template <class K>
+__device__ __forceinline__ K group_key(K first, K second, bool two) {
+  return two && second != 0 ? order_key(key_value(first) + key_value(second)) : first;
+}
+
+// Keys of experts outside the best groups become 0.  value: the key of an expert's part of its
+// group's score, 0 if it cannot be chosen.  `row`: an LDS row of L * PER keys.
+template <int L, int PER, bool NEAR, class V, class K>
+__device__ __forceinline__ void keep_groups(const RouteArgs &g, const V (&value)[PER], uint64_t *lds_row,
+                                            K (&key)[PER], float slack, bool &near) {
+  const int lane = lane_id() & (L - 1), e0 = lane * PER;
+  const bool two = g.group_top == 2;
+  // of the lane's own groups: the lowest key kept, the highest left out
+  V kept = static_cast<V>(~0ull), out = 0;
+  auto place = [&](V mine, int better) {
+    if (better < g.top_groups)
+      kept = mine < kept ? mine : kept;
+    else
+      out = mine > out ? mine : out;
+    return better < g.top_groups;
+  };
+  // lanes that hold a group, where it is a power of two of them
+  const int group_lanes = g.group_size % PER ? 0 : g.group_size / PER;
+  if (group_lanes > 0 && (group_lanes & (group_lanes - 1)) == 0) {
+    V first = 0, second = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const V low = pick(value[i] < first, value[i], first);
+      first = pick(value[i] > first, value[i], first);
+      second = pick(low > second, low, second);
+    }
+    auto merge = [&](auto step) {
+      constexpr int STEP = decltype(step)::value;
+      if (group_lanes <= STEP) return;
+      const V a = partner<STEP>(first), b = partner<STEP>(second);
+      const V low = pick(a < first, a, first), high = pick(second > b, second, b);
+      first = pick(a > first, a, first);
+      second = pick(low > high, low, high);
+    };
+    merge(std::integral_constant<int, 1>());
+    merge(std::integral_constant<int, 2>());
+    merge(std::integral_constant<int, 4>());
+    merge(std::integral_constant<int, 8>());
+    if constexpr (L >= 32) merge(std::integral_constant<int, 16>());
+    if constexpr (L >= 64) merge(std::integral_constant<int, 32>());
+    const V mine = group_key(first, second, two);
+    const int own = lane / group_lanes;
+    int better = 0;
+    for (int h = 0; h < g.groups; ++h) {
+      const V u = lane_value<L>(mine, h * group_lanes);
+      better += u > mine || (u == mine && h < own);
+    }
+    if (own < g.groups && !place(mine, better)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = 0;
+    }
+  } else {
+    V *row = reinterpret_cast<V *>(lds_row);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) row[e0 + i] = value[i];
+    __builtin_amdgcn_wave_barrier();
+    // a group's key takes the place of its first expert's
+    for (int q = lane; q < g.groups; q += L) {
+      V first = 0, second = 0;
+      for (int i = 0; i < g.group_size; ++i) {
+        const V u = row[q * g.group_size + i];
+        const V low = u < first ? u : first;
+        first = u > first ? u : first;
+        second = low > second ? low : second;
+      }
+      row[q * g.group_size] = group_key(first, second, two);
+    }
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = e0 + i;
+      if (e < g.e) {
+        const int q = e / g.group_size;
+        const V mine = row[q * g.group_size];
+        int better = 0;
+        for (int h = 0; h < g.groups; ++h) {
+          const V u = row[h * g.group_size];
+          better += u > mine || (u == mine && h < q);
+        }
+        if (!place(mine, better)) key[i] = 0;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+  if constexpr (NEAR) {
+    kept = ~lanes_best<L>(static_cast<V>(~kept));
+    out = lanes_best<L>(out);
+    if (out != 0) near = near || too_near(key_value(kept), key_value(out), slack);
+  }
+}
+
+// The choices of token t by a whole wave, in 64 bits: lane j gets the j-th expert.
+template <int PER, class T>
+__device__ __forceinline__ int choose64(const RouteArgs &g, int64_t t, uint64_t *lds_row) {
+  const int e0 = lane_id() * PER;
+  float l[PER], b[PER];
+  load_row(static_cast<const T *>(g.logits) + t * g.e, e0, g.e, false, -kInf, l);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) b[i] = 0.0f;
+  if (g.bias) load_row(g.bias, e0, g.e, false, 0.0f, b);
+  double v[PER];
+  scores64<kWave>(l, g.sigmoid, v);
+  uint64_t part[PER], key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    const int e = e0 + i;
-    if (e < g.e) {
-      const int q = e / g.group_size;
-      const uint64_t mine = row[q * g.group_size];
-      int better = 0;
-      for (int h = 0; h < g.groups; ++h) {
-        const uint64_t u = row[h * g.group_size];
-        better += u > mine || (u == mine && h < q);
-      }
-      if (better >= g.top_groups) key[i] = 0;
-    }
+    part[i] = l[i] == -kInf ? 0 : order_key(v[i] + b[i]);
+    key[i] = g.bias ? part[i] : order_key(static_cast<double>(l[i]));
   }
-  __builtin_amdgcn_wave_barrier();
+  bool ignored = false;
+  if (g.groups > 1) keep_groups<kWave, PER, false>(g, part, lds_row, key, 0.0f, ignored);
+  return choose<kWave, PER, false>(key, g.k, 0.0f, ignored);
 }
 
 template <int L, int PER, class T>
@@ -309,91 +484,92 @@ __global__ __launch_bounds__(kThreads) void route_kernel(RouteArgs g) {
   constexpr int kTokens = kThreads / L;
   __shared__ uint64_t rows[kThreads * PER];
   const int lane = lane_id() & (L - 1), e0 = lane * PER, own = threadIdx.x / L;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTokens;
-  // (whole waves go round together)
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < g.n; t0 += stride) {
-    const bool live = t0 + own < g.n;
-    const int64_t t = live ? t0 + own : t0;
-    const T *row = static_cast<const T *>(g.logits) + t * g.e;
-    float l[PER];
-    load_row(row, e0, g.e, g.vector, -kInf, l);
+  uint64_t *mine = rows + own * L * PER;
+  const bool sums = g.groups > 1 && g.group_top == 2;
+  float b[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) b[i] = 0.0f;
+  if (g.bias) load_row(g.bias, e0, g.e, g.vector, 0.0f, b);
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+  const bool live = t0 + own < g.n;
+  const int64_t t = live ? t0 + own : t0;
+  const T *row = static_cast<const T *>(g.logits) + t * g.e;
+  float l[PER];
+  load_row(row, e0, g.e, g.vector, -kInf, l);
 
-    // scores, where something besides the chosen logits needs them
-    float s[PER], inv = 1.0f;
-    const bool stats = g.scores || g.bias || !g.renormalize || g.sigmoid;
-    if (g.sigmoid) {
+  // scores, where something besides the chosen logits needs them
+  float s[PER], inv = 1.0f, top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) s[i] = 0.0f;
+  if (g.sigmoid) {
+    if (g.scores || g.bias || sums) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) s[i] = sigmoid_fine(l[i]);
-    } else if (stats) {
-      inv = softmax_parts<L>(l, s);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) s[i] *= inv;
     }
-    if (g.scores && live) store_row(g.scores + t * g.e, e0, g.e, g.vector, s);
-
-    uint64_t *mine = rows + own * L * PER;
-    const bool sums = g.groups > 1 && g.group_top == 2;
-    double v[PER];
-    if (g.bias || sums) {
-      float b[PER];
+  } else if (g.scores || g.bias || sums || !g.renormalize) {
+    inv = softmax_parts<L>(l, s, top);
 #pragma unroll
-      for (int i = 0; i < PER; ++i) b[i] = 0.0f;
-      if (g.bias) load_row(g.bias, e0, g.e, false, -kInf, b);
-      scores64<L>(l, g.sigmoid, v);
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        v[i] = l[i] == -kInf || e0 + i >= g.e ? -__builtin_inf() : v[i] + b[i];
-    }
-    int id;
-    if (g.bias) {
-      uint64_t key[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = order_key(v[i]);
-      if (g.groups > 1) keep_groups<L>(g, v, mine, key);
-      id = choose<L>(key, g.k);
-    } else {
-      uint32_t key[PER];
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = order_key(l[i]);
-      if (g.groups > 1) {
-        if (!sums) {
-#pragma unroll
-          for (int i = 0; i < PER; ++i) v[i] = l[i];
-        }
-        keep_groups<L>(g, v, mine, key);
-      }
-      id = choose<L>(key, g.k);
-    }
-
-    if (lane < g.k && live) g.ids[t * g.k + lane] = id;
-    if (!g.weights) continue;
-    // lane j: the j-th choice's logit and weight
-    float w = 0.0f;
-    const bool held = lane < g.k && id >= 0;
-    float chosen = -kInf;
-    if (held) chosen = load_one(row + id);
-    if (g.sigmoid) {
-      w = held ? sigmoid_fine(chosen) : 0.0f;
-    } else if (g.renormalize) {
-      float top = lanes_max<L>(chosen);
-      if (top == -kInf) top = 0.0f;
-      w = held ? exp_fine(chosen - top) : 0.0f;
-    } else {
-      // the same bits as the score's
-      float top = -kInf;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) top = fmaxf(top, l[i]);
-      top = lanes_max<L>(top);
-      if (top == -kInf) top = 0.0f;
-      w = held ? exp_fine(chosen - top) * inv : 0.0f;
-    }
-    if (g.renormalize) {
-      const float sum = lanes_sum<L>(w);
-      w = sum == 0.0f ? 0.0f : w / sum;
-    }
-    if (held && inv != inv) w = inv;  // a NaN among the token's logits
-    if (lane < g.k && live) g.weights[t * g.k + lane] = w * g.scale;
+    for (int i = 0; i < PER; ++i) s[i] *= inv;
   }
+  if (g.scores && live) store_row(g.scores + t * g.e, e0, g.e, g.vector, s);
+
+  uint32_t key[PER];
+  bool near = false;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) key[i] = order_key(l[i]);  // 0: not to be chosen
+  int id;
+  if (g.bias || sums) {
+    const float slack = g.sigmoid ? kSigmoidSlack : kSoftmaxSlack;
+    uint32_t part[PER];
+#pragma unroll
+    for (int i = 0; i < PER; ++i) part[i] = pick(key[i] == 0, 0u, order_key(s[i] + b[i]));
+    if (g.bias) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) key[i] = part[i];
+    }
+    if (g.groups > 1) keep_groups<L, PER, true>(g, part, mine, key, slack, near);
+    id = g.bias ? choose<L, PER, true>(key, g.k, slack, near) : choose<L, PER, false>(key, g.k, slack, near);
+    // again in 64 bits, a token at a time
+    const int first = threadIdx.x / kWave * kWave / L;  // the wave's first token in the workgroup
+    for (int q = 0; q < kWave / L; ++q) {
+      const uint64_t m = ballot(near && live && own - first == q);
+      if (m == 0) continue;
+      const int other = choose64<PER * L / kWave, T>(g, t0 + first + q, rows + first * L * PER);
+      const int same = __shfl(other, lane);
+      if (own - first == q) id = same;
+    }
+  } else {
+    if (g.groups > 1) {
+      uint32_t part[PER];
+#pragma unroll
+      for (int i = 0; i < PER; ++i) part[i] = key[i];
+      keep_groups<L, PER, false>(g, part, mine, key, 0.0f, near);
+    }
+    id = choose<L, PER, false>(key, g.k, 0.0f, near);
+  }
+
+  if (lane < g.k && live) g.ids[t * g.k + lane] = id;
+  if (!g.weights) return;
+  // lane j: the j-th choice's logit and weight
+  float w = 0.0f;
+  const bool held = lane < g.k && id >= 0;
+  float chosen = -kInf;
+  if (held) chosen = load_one(row + id);
+  if (g.sigmoid) {
+    w = held ? sigmoid_fine(chosen) : 0.0f;
+  } else if (g.renormalize) {
+    float best = lanes_max<L>(chosen);
+    if (best == -kInf) best = 0.0f;
+    w = held ? exp_fine(chosen - best) : 0.0f;
+  } else {
+    w = held ? exp_fine(chosen - top) * inv : 0.0f;  // the score's bits
+  }
+  if (g.renormalize) {
+    const float sum = lanes_sum<L>(w);
+    w = sum == 0.0f ? 0.0f : w / sum;
+  }
+  if (held && inv != inv) w = inv;  // a NaN among the token's logits
+  if (lane < g.k && live) g.weights[t * g.k + lane] = w * g.scale;
 }
 
 // ------------------------------------------------------ gradient ---
@@ -415,118 +591,117 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteGradArgs 
   __shared__ float rows[kThreads * PER];
   const int lane = lane_id() & (L - 1), e0 = lane * PER, own = threadIdx.x / L;
   float *add = rows + own * L * PER;
-  const int64_t stride = static_cast<int64_t>(gridDim.x) * kTokens;
   // whether a gradient reaches experts that were not chosen
   const bool whole = g.dscores || (!g.sigmoid && !g.renormalize);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens; t0 < g.n; t0 += stride) {
-    const bool live = t0 + own < g.n;
-    const int64_t t = live ? t0 + own : t0;
-    const T *row = static_cast<const T *>(g.logits) + t * g.e;
-    float l[PER], s[PER], d[PER];
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTokens;
+  const bool live = t0 + own < g.n;
+  const int64_t t = live ? t0 + own : t0;
+  const T *row = static_cast<const T *>(g.logits) + t * g.e;
+  float l[PER], s[PER], d[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = d[i] = 0.0f;
-    if (whole) {
-      load_row(row, e0, g.e, g.vector, -kInf, l);
-      if (g.dscores) load_row(g.dscores + t * g.e, e0, g.e, g.vector, 0.0f, d);
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) add[e0 + i] = 0.0f;
-    if (g.dweights) {
-      // lane j: the j-th choice
-      int id = lane < g.k ? g.ids[t * g.k + lane] : -1;
-      const bool held = id >= 0 && id < g.e;
-      if (!held) id = -1;
-      float u = held ? g.dweights[t * g.k + lane] * g.scale : 0.0f;
-      float chosen = -kInf;
-      if (held) chosen = load_one(row + id);
-      const float sj = g.sigmoid && held ? sigmoid_fine(chosen) : 0.0f;
-      if (g.renormalize) {
-        float w = sj;
-        if (!g.sigmoid) {
-          float top = lanes_max<L>(chosen);
-          if (top == -kInf) top = 0.0f;
-          w = held ? exp_fine(chosen - top) : 0.0f;
-        }
-        const float sum = lanes_sum<L>(w);
-        w = sum == 0.0f ? 0.0f : w / sum;
-        const float dot = lanes_sum<L>(u * w);
-        u = held ? w * (u - dot) : 0.0f;
-        if (g.sigmoid) u *= 1.0f - sj;
-      } else if (g.sigmoid) {
-        u *= sj * (1.0f - sj);
-      }
-      // an ID that repeats within the token: its first lane adds up all
-      float total = 0.0f;
-      bool first = held;
-      for (int j = 0; j < g.k; ++j) {
-        const int other_id = __shfl(id, j, L);
-        const float other_u = __shfl(u, j, L);
-        if (other_id == id) {
-          total += other_u;
-          if (j < lane) first = false;
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
-      if (first) add[id] = total;
-      __builtin_amdgcn_wave_barrier();
-    }
-    float out[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) out[i] = add[e0 + i];
-    __builtin_amdgcn_wave_barrier();
-    if (whole) {
-      if (g.sigmoid) {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          const float p = sigmoid_fine(l[i]);
-          out[i] += d[i] * p * (1.0f - p);
-        }
-      } else {
-        const float inv = softmax_parts<L>(l, s);
-        float dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-          s[i] *= inv;
-          if (!g.renormalize) {
-            d[i] += out[i];
-            out[i] = 0.0f;
-          }
-          dot += e0 + i < g.e ? d[i] * s[i] : 0.0f;
-        }
-        dot = lanes_sum<L>(dot);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) out[i] += s[i] * (d[i] - dot);
-      }
-    }
-    if (live) store_row(static_cast<T *>(g.dlogits) + t * g.e, e0, g.e, g.vector, out);
+  for (int i = 0; i < PER; ++i) s[i] = d[i] = 0.0f;
+  if (whole) {
+    load_row(row, e0, g.e, g.vector, -kInf, l);
+    if (g.dscores) load_row(g.dscores + t * g.e, e0, g.e, g.vector, 0.0f, d);
   }
+#pragma unroll
+  for (int i = 0; i < PER; ++i) add[e0 + i] = 0.0f;
+  if (g.dweights) {
+    // lane j: the j-th choice
+    int id = lane < g.k ? g.ids[t * g.k + lane] : -1;
+    const bool held = id >= 0 && id < g.e;
+    if (!held) id = -1;
+    float u = held ? g.dweights[t * g.k + lane] * g.scale : 0.0f;
+    float chosen = -kInf;
+    if (held) chosen = load_one(row + id);
+    const float sj = g.sigmoid && held ? sigmoid_fine(chosen) : 0.0f;
+    if (g.renormalize) {
+      float w = sj;
+      if (!g.sigmoid) {
+        float top = lanes_max<L>(chosen);
+        if (top == -kInf) top = 0.0f;
+        w = held ? exp_fine(chosen - top) : 0.0f;
+      }
+      const float sum = lanes_sum<L>(w);
+      w = sum == 0.0f ? 0.0f : w / sum;
+      const float dot = lanes_sum<L>(u * w);
+      u = held ? w * (u - dot) : 0.0f;
+      if (g.sigmoid) u *= 1.0f - sj;
+    } else if (g.sigmoid) {
+      u *= sj * (1.0f - sj);
+    }
+    // an ID that repeats within the token: its first lane adds up all
+    float total = 0.0f;
+    bool first = held;
+    for (int j = 0; j < g.k; ++j) {
+      const int other_id = __shfl(id, j, L);
+      const float other_u = __shfl(u, j, L);
+      if (other_id == id) {
+        total += other_u;
+        if (j < lane) first = false;
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    if (first) add[id] = total;
+    __builtin_amdgcn_wave_barrier();
+  }
+  float out[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) out[i] = add[e0 + i];
+  __builtin_amdgcn_wave_barrier();
+  if (whole) {
+    if (g.sigmoid) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const float p = sigmoid_fine(l[i]);
+        out[i] += d[i] * p * (1.0f - p);
+      }
+    } else {
+      float top;
+      const float inv = softmax_parts<L>(l, s, top);
+      float dot = 0.0f;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        s[i] *= inv;
+        if (!g.renormalize) {
+          d[i] += out[i];
+          out[i] = 0.0f;
+        }
+        dot += e0 + i < g.e ? d[i] * s[i] : 0.0f;
+      }
+      dot = lanes_sum<L>(dot);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) out[i] += s[i] * (d[i] - dot);
+    }
+  }
+  if (live) store_row(static_cast<T *>(g.dlogits) + t * g.e, e0, g.e, g.vector, out);
 }
 
 // f(integral_constant<L>, integral_constant<PER>): the lanes of a token and the experts of
-// a lane that E experts and k choices need.
-template <class F>
+// a lane that E experts and k choices need.  The choice is bound by its instructions, of which
+// whole waves with four keys a lane need the fewest past 128 experts (8192 tokens,
+// 256 experts: 16 lanes of 16 keys 24.8 us, 64 of 4 16.5); the gradient by its loads, of which few
+// lanes have more in flight (16384 tokens, 128 experts: 16 lanes of 8 6.3 us, 32 of 4 7.5).
+template <bool BACKWARD, class F>
 hipError_t with_lanes(int e, int k, F f) {
-  auto at = [&](auto l, auto per) { return f(l, per); };
   typedef std::integral_constant<int, 4> Four;
   typedef std::integral_constant<int, 8> Eight;
   typedef std::integral_constant<int, 16> Sixteen;
   typedef std::integral_constant<int, 64> All;
-  if (k <= 16 && e <= 256) {
-    if (e <= 64) return at(Sixteen(), Four());
-    if (e <= 128) return at(Sixteen(), Eight());
-    return at(Sixteen(), Sixteen());
+  if (e <= 64 && k <= 16) return f(Sixteen(), Four());
+  if constexpr (BACKWARD) {
+    if (e <= 128 && k <= 16) return f(Sixteen(), Eight());
+    if (e <= 256 && k <= 16) return f(Sixteen(), Sixteen());
+  } else {
+    if (e <= 128 && k <= 32) return f(std::integral_constant<int, 32>(), Four());
   }
-  if (e <= 256) return at(All(), Four());
-  if (e <= 512) return at(All(), Eight());
-  return at(All(), Sixteen());
+  if (e <= 256) return f(All(), Four());
+  if (e <= 512) return f(All(), Eight());
+  return f(All(), Sixteen());
 }
 
-// Workgroups: a round of the whole device at most, which then go on.
-constexpr int64_t kMostBlocks = 1 << 20;
-inline uint32_t token_blocks(int64_t n, int tokens) {
-  const int64_t b = (n + tokens - 1) / tokens;
-  return static_cast<uint32_t>(b < kMostBlocks ? b : kMostBlocks);
-}
+// Tokens of one launch (a launch's threads fit 32 bits): more take several.
+constexpr int64_t kLaunchTokens = 1 << 22;
 
 // Rows of e values that start, like the arrays, on whole vectors of four.
 inline bool whole_vectors(int e, std::initializer_list<const void *> f32, std::initializer_list<const void *> t,
@@ -555,19 +730,26 @@ hipError_t launch_route(const moe_problem &p, const moe_router &r, const void *l
   g.groups = r.top_groups < r.n_groups ? r.n_groups : 1;  // all groups kept: no choice to make
   g.group_size = p.n_experts / g.groups;
   g.top_groups = r.top_groups;
-  // (a group of one expert has no second)
   g.group_top = r.group_top;
   g.sigmoid = r.score == MOE_SCORE_SIGMOID;
   g.renormalize = r.renormalize != 0;
-  g.vector = whole_vectors(g.e, {scores}, {logits}, bf16);
+  g.vector = whole_vectors(g.e, {scores, bias}, {logits}, bf16);
   g.scale = r.scale;
-  return with_lanes(g.e, g.k, [&](auto l, auto per) {
-    constexpr int L = decltype(l)::value, PER = decltype(per)::value;
-    const uint32_t grid = token_blocks(g.n, kThreads / L);
-    if (bf16)
-      route_kernel<L, PER, uint16_t><<<grid, kThreads, 0, stream>>>(g);
-    else
-      route_kernel<L, PER, float><<<grid, kThreads, 0, stream>>>(g);
+  return with_lanes<false>(g.e, g.k, [&](auto l, auto per) {
+    constexpr int L = decltype(l)::value, PER = decltype(per)::value, kTokens = kThreads / L;
+    for (int64_t from = 0; from < p.n_tokens; from += kLaunchTokens) {
+      RouteArgs part = g;
+      part.n = p.n_tokens - from < kLaunchTokens ? p.n_tokens - from : kLaunchTokens;
+      part.logits = static_cast<const char *>(logits) + from * g.e * (bf16 ? 2 : 4);
+      part.ids += from * g.k;
+      if (weights) part.weights += from * g.k;
+      if (scores) part.scores += from * g.e;
+      const uint32_t grid = static_cast<uint32_t>((part.n + kTokens - 1) / kTokens);
+      if (bf16)
+        route_kernel<L, PER, uint16_t><<<grid, kThreads, 0, stream>>>(part);
+      else
+        route_kernel<L, PER, float><<<grid, kThreads, 0, stream>>>(part);
+    }
     return hipGetLastError();
   });
 }
@@ -590,13 +772,22 @@ hipError_t launch_route_backward(const moe_problem &p, const moe_router &r, cons
   g.renormalize = r.renormalize != 0;
   g.vector = whole_vectors(g.e, {dscores}, {logits, dlogits}, bf16);
   g.scale = r.scale;
-  return with_lanes(g.e, g.k, [&](auto l, auto per) {
-    constexpr int L = decltype(l)::value, PER = decltype(per)::value;
-    const uint32_t grid = token_blocks(g.n, kThreads / L);
-    if (bf16)
-      route_backward_kernel<L, PER, uint16_t><<<grid, kThreads, 0, stream>>>(g);
-    else
-      route_backward_kernel<L, PER, float><<<grid, kThreads, 0, stream>>>(g);
+  return with_lanes<true>(g.e, g.k, [&](auto l, auto per) {
+    constexpr int L = decltype(l)::value, PER = decltype(per)::value, kTokens = kThreads / L;
+    for (int64_t from = 0; from < p.n_tokens; from += kLaunchTokens) {
+      RouteGradArgs part = g;
+      part.n = p.n_tokens - from < kLaunchTokens ? p.n_tokens - from : kLaunchTokens;
+      part.logits = static_cast<const char *>(logits) + from * g.e * (bf16 ? 2 : 4);
+      part.dlogits = static_cast<char *>(dlogits) + from * g.e * (bf16 ? 2 : 4);
+      if (ids) part.ids += from * g.k;
+      if (dweights) part.dweights += from * g.k;
+      if (dscores) part.dscores += from * g.e;
+      const uint32_t grid = static_cast<uint32_t>((part.n + kTokens - 1) / kTokens);
+      if (bf16)
+        route_backward_kernel<L, PER, uint16_t><<<grid, kThreads, 0, stream>>>(part);
+      else
+        route_backward_kernel<L, PER, float><<<grid, kThreads, 0, stream>>>(part);
+    }
     return hipGetLastError();
   });
 }
