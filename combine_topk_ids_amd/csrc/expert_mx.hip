@@ -37,30 +37,6 @@ struct MxGateUpRow {
   }
 };
 
-__device__ __forceinline__ float activate(int act, float z) {
-  switch (act) {
-    case MOE_ACT_SILU: return act_value<MOE_ACT_SILU>(z);
-    case MOE_ACT_GELU_TANH: return act_value<MOE_ACT_GELU_TANH>(z);
-    case MOE_ACT_RELU: return act_value<MOE_ACT_RELU>(z);
-    default: return z;
-  }
-}
-
-// As with_blocks; a tile of six blocks a wave goes by single ones.
-template <class S, class F>
-__device__ __forceinline__ void with_own_blocks(int rows, F f) {
-  if constexpr (S::FI == 6) {
-    const int blocks = (rows + 16 * S::WI - 1) / (16 * S::WI);
-    if (blocks <= 2) return f(std::integral_constant<int, 2>());
-    if (blocks == 3) return f(std::integral_constant<int, 3>());
-    if (blocks == 4) return f(std::integral_constant<int, 4>());
-    if (blocks == 5) return f(std::integral_constant<int, 5>());
-    return f(std::integral_constant<int, 6>());
-  } else {
-    with_blocks<S>(rows, f);
-  }
-}
-
 template <class S, bool GLU>
 __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kernel(MxArgs g) {
   __shared__ __align__(1024) char smem[S::kLdsBytes];
@@ -78,11 +54,10 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
 
   typedef typename std::conditional<GLU, MxGateUpRow, SameRow>::type WeightRow;
   MxFeed<S, WeightRow> feed;
-  if constexpr (GLU) feed.j.row.n = feed.w.row.n = g.n;
+  if constexpr (GLU) feed.j.row.n = g.n;
   feed.i.init(x_bytes);
   feed.j.init(w_bytes);
-  feed.x.init(x_scale_bytes);
-  feed.w.init(blocks);
+  feed.s.init(x_scale_bytes, blocks, feed.j.row);
   auto source = [&](const RowTile &r) {
     if (r.e < 0) return kNoMxSource;
     const int j0 = r.j * kCols, left = min(r.count - r.i0, S::BI);
@@ -103,17 +78,19 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
   start_mx<S>(lds, feed, cur, at);
   auto one_tile = [&](auto own_blocks) {
     constexpr int FI = decltype(own_blocks)::value;
-    constexpr int kTurnCols = GLU ? kWaveCols : S::kTurnCols, kTurns = kWaveCols / kTurnCols;
-    constexpr int kTurnBlocks = kTurnCols / 16;
+    constexpr int kHalves = GLU ? 2 : 1;             // blocks of z to one of y
+    constexpr int kPairs = S::FJ / kHalves / 2;      // of blocks of y
+    static_assert(kPairs * 2 * kHalves == S::FJ, "y leaves by pairs of blocks");
     f32x4 acc[FI][S::FJ];
     multiply_mx<S, FI>(lds, feed, cur, following, blocks, at, acc);
     const int lane = late_lane_id();
     if constexpr (S::WK > 1) {
-      // the groups' sums, added in order by the first, through what is its way out
-      lds_ptr sums = lds + S::kLoadLds + lane * 16;
+      // the groups' sums, added in order by the first
+      lds_ptr sums = (lds_ptr)smem + S::WK * S::kGroupLds + lane * 16;
       if (group_id<S>() > 0) {
 #pragma unroll
-        for (int b = 0; b < S::FJ; ++b) *(MOE_LDS f32x4 *)(sums + b * kWave * 16) = acc[0][b];
+        for (int b = 0; b < S::FJ; ++b)
+          *(MOE_LDS f32x4 *)(sums + (group_id<S>() - 1) * S::kSums + b * kWave * 16) = acc[0][b];
       }
       __syncthreads();
       if (group_id<S>() > 0) {
@@ -124,9 +101,8 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
       for (int q = 1; q < S::WK; ++q)
 #pragma unroll
         for (int b = 0; b < S::FJ; ++b)
-          acc[0][b] += *(MOE_LDS const f32x4 *)(sums + q * S::kGroupLds + b * kWave * 16);
+          acc[0][b] += *(MOE_LDS const f32x4 *)(sums + (q - 1) * S::kSums + b * kWave * 16);
     }
-    const Transpose<kTurnCols> turn{lds + S::kLoadLds + group_wave<S>() * Transpose<kTurnCols>::kBytes, lane};
     const float *bias = g.bias ? g.bias + static_cast<int64_t>(t.e) * wrows : nullptr;
     const int col0 = t.j * kCols + w.wj * kWaveCols;  // of the wave
     const int left = t.count - t.i0;                  // rows of the tile
@@ -138,87 +114,94 @@ __global__ __launch_bounds__(S::kThreads *S::WK, S::kWavesPerSimd) void mx_kerne
       shift[b] = bias && c < g.n ? *reinterpret_cast<const f32x4 *>(bias + (GLU && b % 2 ? g.n : 0) + c)
                                  : f32x4{0.f, 0.f, 0.f, 0.f};
     }
-    // where pass p of block row a goes: row and column of its eight values; past the
-    // results' end kNowhere
-    auto row_of = [&](int a, int p) { return (w.wi + a * S::WI) * 16 + turn.row(p); };
-    auto place = [&](int a, int p, int h) {
-      const int i = row_of(a, p), col = col0 + h * kTurnCols + turn.col();
+    // A lane has 4 neighbouring columns of each block of y.  Lanes 16 apart exchange those of two
+    // blocks, and each has 8 of one: 16 bytes of bf16, a quarter of the pair's 32 columns.
+    const int i_lane = lane & 15, quarter = lane >> 4;
+    const int col_lane = col0 + (quarter & 1) * 16 + (quarter >> 1) * 8;
+    // place of the lane's values of pair h, block row a: past the results' end kNowhere
+    auto place = [&](int a, int h) {
+      const int i = (w.wi + a * S::WI) * 16 + i_lane, col = col_lane + h * 32;
       return i < left && col < g.n ? static_cast<uint32_t>(i * g.n + col) : kNowhere;
     };
-    auto in_bytes = [](uint32_t at, int shift_left) { return at == kNowhere ? kNowhere : at << shift_left; };
+    auto in_bytes = [](uint32_t at) { return static_cast<int>(at == kNowhere ? at : at * 2); };
     // all of the residual before the first store: one trip to memory
-    uint4 add[GLU ? 1 : FI][kTurns][turn.kPasses];
+    uint4 add[GLU ? 1 : FI][kPairs];
     if constexpr (!GLU) {
       if (g.residual) {
         const auto r = buffer_rsrc(g.residual + row0 * g.n, kRecords);
 #pragma unroll
         for (int a = 0; a < FI; ++a)
 #pragma unroll
-          for (int h = 0; h < kTurns; ++h)
-#pragma unroll
-            for (int p = 0; p < turn.kPasses; ++p)
-              add[a][h][p] = __builtin_bit_cast(
-                  uint4, __builtin_amdgcn_raw_buffer_load_b128(
-                             r, static_cast<int>(in_bytes(place(a, p, h), 1)), 0, kLoadDefault));
+          for (int h = 0; h < kPairs; ++h)
+            add[a][h] = __builtin_bit_cast(
+                uint4, __builtin_amdgcn_raw_buffer_load_b128(r, in_bytes(place(a, h)), 0, kLoadDefault));
       }
     }
+    auto leave = [&](auto act) {
+      constexpr int ACT = decltype(act)::value;
 #pragma unroll
-    for (int a = 0; a < FI; ++a) {
+      for (int a = 0; a < FI; ++a) {
 #pragma unroll
-      for (int b = 0; b < S::FJ; ++b) acc[a][b] += shift[b];
+        for (int b = 0; b < S::FJ; ++b) acc[a][b] += shift[b];
 #pragma unroll
-      for (int h = 0; h < kTurns; ++h) {
+        for (int h = 0; h < kPairs; ++h) {
+          float v[8];
 #pragma unroll
-        for (int b = 0; b < kTurnBlocks; ++b) {
-          const int at_b = (h * kTurnBlocks + b) * (GLU ? 2 : 1);
-          f32x4 y;
+          for (int c = 0; c < 4; ++c) {
+            uint32_t y[2];
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            y[c] = activate(g.act, acc[a][at_b][c]) * (GLU ? acc[a][at_b + (GLU ? 1 : 0)][c] : 1.0f);
-          turn.put(b, y);
-        }
-        __builtin_amdgcn_wave_barrier();
-        if (GLU && g.codes) {
-          const auto rc = buffer_rsrc(g.codes + row0 * (g.n / 2), kRecords);
-          const auto rs = buffer_rsrc(g.scales + row0 * (g.n / 32), kRecords);
-#pragma unroll
-          for (int p = 0; p < turn.kPasses; ++p) {
-            float v[8];
-            turn.get(p, v);
+            for (int u = 0; u < 2; ++u) {
+              const int b = (h * 2 + u) * kHalves;
+              y[u] = __float_as_uint(act_value<ACT>(acc[a][b][c]) * (GLU ? acc[a][b + kHalves - 1][c] : 1.0f));
+            }
+            // odd rows of 16 lanes of the first change places with even rows of the second
+            const auto p = __builtin_amdgcn_permlane16_swap(y[0], y[1], false, false);
+            const uint32_t x0 = p[0], x1 = p[1];
+            v[c] = __uint_as_float(x0);
+            v[c + 4] = __uint_as_float(x1);
+          }
+          const uint32_t to = place(a, h);
+          if (GLU && g.codes) {
+            // a row's 32 columns are in four lanes, 16 apart
+            uint32_t am = mx_lane_max(v);
+            const auto p = __builtin_amdgcn_permlane16_swap(am, am, false, false);
+            am = max(static_cast<uint32_t>(p[0]), static_cast<uint32_t>(p[1]));
+            const auto p2 = __builtin_amdgcn_permlane32_swap(am, am, false, false);
+            am = max(static_cast<uint32_t>(p2[0]), static_cast<uint32_t>(p2[1]));
             uint32_t scale;
-            const uint32_t c = mx_encode8(v, scale);  // (n is a multiple of 32: whole blocks are in or out)
-            const uint32_t to = place(a, p, h);
+            const uint32_t c = mx_encode8(v, am, scale);  // (n is a multiple of 32: whole blocks are in or out)
+            const auto rc = buffer_rsrc(g.codes + row0 * (g.n / 2), kRecords);
+            const auto rs = buffer_rsrc(g.scales + row0 * (g.n / 32), kRecords);
             __builtin_amdgcn_raw_buffer_store_b32(c, rc, static_cast<int>(to == kNowhere ? to : to / 2), 0, 0);
-            const bool leads = to != kNowhere && (lane & 3) == 0;
+            const bool leads = to != kNowhere && quarter == 0;
             __builtin_amdgcn_raw_buffer_store_b8(static_cast<uint8_t>(scale), rs,
                                                  static_cast<int>(leads ? to / 32 : kNowhere), 0, 0);
-          }
-        } else {
-          const auto r = buffer_rsrc(g.y + row0 * g.n, kRecords);
-#pragma unroll
-          for (int p = 0; p < turn.kPasses; ++p) {
-            float v[8];
-            turn.get(p, v);
+          } else {
             if constexpr (!GLU) {
               if (g.residual) {
                 float more[8];
-                unpack8(add[a][h][p], more);
+                unpack8(add[a][h], more);
 #pragma unroll
                 for (int c = 0; c < 8; ++c) v[c] += more[c];
               }
             }
-            store8(r, in_bytes(place(a, p, h), 1), v);
+            store8(buffer_rsrc(g.y + row0 * g.n, kRecords), static_cast<uint32_t>(in_bytes(to)), v);
           }
         }
-        __builtin_amdgcn_wave_barrier();
       }
+    };
+    switch (g.act) {
+      case MOE_ACT_SILU: leave(std::integral_constant<int, MOE_ACT_SILU>()); break;
+      case MOE_ACT_GELU_TANH: leave(std::integral_constant<int, MOE_ACT_GELU_TANH>()); break;
+      case MOE_ACT_RELU: leave(std::integral_constant<int, MOE_ACT_RELU>()); break;
+      default: leave(std::integral_constant<int, MOE_ACT_NONE>());
     }
-    at.younger = FI * kTurns * turn.kPasses;
+    at.younger = FI * kPairs;
   };
   for (int n = 1; t.e >= 0; ++n) {
     const RowTile next = order.find(n);
     following = source(next);
-    with_own_blocks<S>(t.count - t.i0, one_tile);
+    with_blocks<S>(t.count - t.i0, one_tile);
     t = next;
     cur = following;
   }
@@ -235,27 +218,51 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
   return hipGetLastError();
 }
 
+// Which tile, by the rows an expert has on average, the contraction's length and whether larger
+// tiles would leave compute units without work.  MX-FP4 rows: 128 x 128 and, for many rows, 256 x 256.
+// FP8 rows, whose split into two halves is vector work that a wave does once for all its columns:
+// 64 x 128 in four waves of 16 x 128, and 128 x 256 in eight of 32 x 128 (that in waves of 64 x 64:
+// 24576 rows, K = 2048, N = 4096, 64 experts 451 us against 390).  Measured, us a call, gated, K = 4096,
+// F = 1024, 64 experts:
+//   rows an expert           0.1     4*     12**   16     24     48    128    192    384***
+//   16 x 64, K in four       8.2   674.6    81.8   65.5   83.1  128.6  304.8  447.5  1738
+//   16 x 64                 15.8   612.0    51.8   63.6   81.3  131.5  311.7  475.0  2068
+//   128 x 128               14.8   680.8    62.2   54.8   55.9   60.5   89.5  103.1   332
+//   256 x 256               21.5   832.3    72.2   65.2   66.1   68.6   80.3   90.6   281
+//   FP8: 16 x 64, K in four 11.2   909.6           92.7         145.6^        690.9
+//        16 x 64            20.2   640.2           78.7         110.7^        520.2
+//        64 x 128           27.6   887.5           69.6          72.7^        225.2
+//        128 x 256          54.1  1406.3          109.8         110.4^        213.0
+// (* K = 7168, F = 2048, 256 experts; ** linear, K = 2048, N = 4096; *** F = 2048; ^ 32 rows; 96: 133.8
+// of 64 x 128, 114.4 of 128 x 256.)
+// A tile of 16 rows is one wave with two stages, so that a compute unit holds six and the
+// weights, which pass once, never wait for one barrier (three stages a wave, four waves with a common
+// one: 926 us for 640 above).  Where tiles are few the time is that of one chain of steps, and a long
+// contraction goes to the four waves of a workgroup.
+// A short contraction does not pay for 256 x 256's first loads and last stores (256 rows, N = 4096, 128
+// x 128 and 256 x 256: K = 512 59.7 / 61.8, 1024 81.9 / 81.7, 2048 131.0 / 125.8; linear, N = 7168, K = 1024
+// 84.6 / 90.6), nor does one whose rows (K / 2 bytes) start inside a line: of each the two lines
+// that a step touches come twice, more often than the caches keep them (256 rows, N = 4096,
+// K = 4128 471 / 549).
 template <bool GLU, bool FP8, bool ODD>
 hipError_t launch_sized(const MxArgs &g, int64_t pairs, hipStream_t stream) {
-  typedef MxShape<16, 64, 1, 1, FP8 ? 2 : 3, FP8, ODD, 4> Split;
-  typedef MxShape<16, 64, 1, 1, 4, FP8, ODD> Few;
-  typedef MxShape<64, 128, 2, 2, 3, FP8, ODD> Low;
-  typedef MxShape<128, 128, 2, 2, 2, FP8, ODD> Some;
-  typedef typename std::conditional<FP8, MxShape<128, 256, 2, 4, 2, FP8, ODD>,
-                                    MxShape<256, 256, 2, 4, 2, FP8, ODD>>::type Many;
-  typedef MxShape<FP8 ? 128 : 384, FP8 ? 256 : 128, FP8 ? 2 : 4, FP8 ? 4 : 2, 2, FP8, ODD> Tall;
+  typedef MxShape<16, 64, 1, 1, FP8 ? 2 : 3, FP8, ODD, true, 4> Split;
+  typedef MxShape<16, 64, 1, 1, 2, FP8, ODD, true> Few;
+  typedef typename std::conditional<FP8, MxShape<64, 128, 4, 1, 2, FP8, ODD, false>,
+                                    MxShape<128, 128, 2, 2, 2, FP8, ODD, false>>::type Some;
+  typedef typename std::conditional<FP8, MxShape<128, 256, 4, 2, 2, FP8, ODD, false>,
+                                    MxShape<256, 256, 2, 4, 2, FP8, ODD, false>>::type Many;
   const int64_t used = pairs < g.n_experts ? pairs : g.n_experts, rows = (pairs + used - 1) / used;
   const int wrows = g.n * (GLU ? 2 : 1);
-  const int64_t tiles = row_tile_bound<Some::BI>(pairs, g.n_experts) * col_tiles<Some::BJ>(wrows);
   const int64_t split_tiles = row_tile_bound<Split::BI>(pairs, g.n_experts) * col_tiles<Split::BJ>(wrows);
-  if (g.k >= 2048 && (rows <= 12 || split_tiles <= 2 * kComputeUnits)) return launch<Split, GLU>(g, pairs, stream);
-  if (rows <= 16 && tiles < 4 * kComputeUnits) return launch<Few, GLU>(g, pairs, stream);
-  if (tiles < kEnoughTiles) return launch<Low, GLU>(g, pairs, stream);
-  if (rows <= 112) return launch<Some, GLU>(g, pairs, stream);
-  if (!FP8 && rows < 336) return launch<Tall, GLU>(g, pairs, stream);
-  if (row_tile_bound<Many::BI>(pairs, g.n_experts) * col_tiles<Many::BJ>(wrows) < kEnoughTiles)
-    return launch<Some, GLU>(g, pairs, stream);
-  return launch<Many, GLU>(g, pairs, stream);
+  const int64_t many_tiles = row_tile_bound<Many::BI>(pairs, g.n_experts) * col_tiles<Many::BJ>(wrows);
+  if (g.k >= 2048 && split_tiles <= 2 * kComputeUnits) return launch<Split, GLU>(g, pairs, stream);
+  if (rows <= 12) return launch<Few, GLU>(g, pairs, stream);
+  if constexpr (!ODD) {
+    const bool deep = FP8 || g.k >= 1536;
+    if (rows > (FP8 ? 80 : 112) && deep && many_tiles >= kEnoughTiles) return launch<Many, GLU>(g, pairs, stream);
+  }
+  return launch<Some, GLU>(g, pairs, stream);
 }
 
 template <bool GLU>

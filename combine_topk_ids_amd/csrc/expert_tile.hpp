@@ -129,35 +129,37 @@ __device__ __forceinline__ i32x4 resource(const void *base, uint32_t bytes) {
 // its prefetch to that).  These loads have no register results; what waits for them
 // is wait_and_meet.  First line: scalars written by a vector instruction just before
 // need five cycles; after a write of m0, one.
-#define MOE_TO_LDS(N) \
-  "s_add_u32 m0, m0, %[stride]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o" #N "], %[r], 0 offen lds\n\t"
-#define MOE_TO_LDS_FIRST \
-  "s_nop 4\n\ts_mov_b32 m0, %[to]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o0], %[r], 0 offen lds\n\t"
-template <int STRIDE, int L>
+#define MOE_TO_LDS(N, P) \
+  "s_add_u32 m0, m0, %[stride]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o" #N "], %[r], 0 offen" P " lds\n\t"
+#define MOE_TO_LDS_FIRST(P) \
+  "s_nop 4\n\ts_mov_b32 m0, %[to]\n\ts_nop 0\n\tbuffer_load_dwordx4 %[o0], %[r], 0 offen" P " lds\n\t"
+#define MOE_LOADS_TO_LDS(P)                                                                                       \
+  if constexpr (L == 1)                                                                                           \
+    asm volatile(MOE_TO_LDS_FIRST(P)::[o0] "v"(o[0]), [r] "s"(r), [to] "s"(at) : "memory", "m0", "scc");          \
+  if constexpr (L == 2)                                                                                           \
+    asm volatile(MOE_TO_LDS_FIRST(P) MOE_TO_LDS(1, P)::[o0] "v"(o[0]), [o1] "v"(o[1]), [r] "s"(r), [to] "s"(at),  \
+                 [stride] "n"(STRIDE)                                                                             \
+                 : "memory", "m0", "scc");                                                                        \
+  if constexpr (L == 4)                                                                                           \
+    asm volatile(MOE_TO_LDS_FIRST(P) MOE_TO_LDS(1, P) MOE_TO_LDS(2, P) MOE_TO_LDS(3, P)::[o0] "v"(o[0]),          \
+                 [o1] "v"(o[1]), [o2] "v"(o[2]), [o3] "v"(o[3]), [r] "s"(r), [to] "s"(at), [stride] "n"(STRIDE)   \
+                 : "memory", "m0", "scc");                                                                        \
+  if constexpr (L == 8)                                                                                           \
+    asm volatile(MOE_TO_LDS_FIRST(P) MOE_TO_LDS(1, P) MOE_TO_LDS(2, P) MOE_TO_LDS(3, P) MOE_TO_LDS(4, P)          \
+                     MOE_TO_LDS(5, P) MOE_TO_LDS(6, P) MOE_TO_LDS(7, P)::[o0] "v"(o[0]), [o1] "v"(o[1]),          \
+                 [o2] "v"(o[2]), [o3] "v"(o[3]), [o4] "v"(o[4]), [o5] "v"(o[5]), [o6] "v"(o[6]), [o7] "v"(o[7]),  \
+                 [r] "s"(r), [to] "s"(at), [stride] "n"(STRIDE)                                                   \
+                 : "memory", "m0", "scc");
+// NT: past the caches (what is read once).
+template <int STRIDE, bool NT = false, int L>
 __device__ __forceinline__ void load_lds16(i32x4 r, lds_ptr to, const uint32_t (&o)[L]) {
-  static_assert(L == 1 || L == 2 || L == 4 || L == 6 || L == 8, "whole groups");
+  static_assert(L == 1 || L == 2 || L == 4 || L == 8, "whole groups");
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<size_t>(to)));
-  if constexpr (L == 1)
-    asm volatile(MOE_TO_LDS_FIRST ::[o0] "v"(o[0]), [r] "s"(r), [to] "s"(at) : "memory", "m0", "scc");
-  if constexpr (L == 2)
-    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1)::[o0] "v"(o[0]), [o1] "v"(o[1]), [r] "s"(r), [to] "s"(at),
-                 [stride] "n"(STRIDE)
-                 : "memory", "m0", "scc");
-  if constexpr (L == 4)
-    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3)::[o0] "v"(o[0]), [o1] "v"(o[1]),
-                 [o2] "v"(o[2]), [o3] "v"(o[3]), [r] "s"(r), [to] "s"(at), [stride] "n"(STRIDE)
-                 : "memory", "m0", "scc");
-  if constexpr (L == 6)
-    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3) MOE_TO_LDS(4) MOE_TO_LDS(5)::[o0] "v"(o[0]),
-                 [o1] "v"(o[1]), [o2] "v"(o[2]), [o3] "v"(o[3]), [o4] "v"(o[4]), [o5] "v"(o[5]), [r] "s"(r),
-                 [to] "s"(at), [stride] "n"(STRIDE)
-                 : "memory", "m0", "scc");
-  if constexpr (L == 8)
-    asm volatile(MOE_TO_LDS_FIRST MOE_TO_LDS(1) MOE_TO_LDS(2) MOE_TO_LDS(3) MOE_TO_LDS(4) MOE_TO_LDS(5)
-                     MOE_TO_LDS(6) MOE_TO_LDS(7)::[o0] "v"(o[0]), [o1] "v"(o[1]), [o2] "v"(o[2]),
-                 [o3] "v"(o[3]), [o4] "v"(o[4]), [o5] "v"(o[5]), [o6] "v"(o[6]), [o7] "v"(o[7]), [r] "s"(r),
-                 [to] "s"(at), [stride] "n"(STRIDE)
-                 : "memory", "m0", "scc");
+  if constexpr (NT) {
+    MOE_LOADS_TO_LDS(" nt")
+  } else {
+    MOE_LOADS_TO_LDS("")
+  }
 }
 __device__ __forceinline__ void load_lds4(i32x4 r, lds_ptr to, uint32_t o) {
   const uint32_t at = __builtin_amdgcn_readfirstlane(static_cast<uint32_t>(reinterpret_cast<size_t>(to)));
@@ -178,7 +180,7 @@ constexpr Operand kNoOperand{nullptr, 0, 0};
 
 // Rows of `row_bytes` stored along c.  ROW(r) maps a tile row to a row of the
 // operand (it must satisfy ROW(a * kLoadRows + b) = ROW(a * kLoadRows) + ROW(b), b < kLoadRows).
-template <class S, int L, class ROW>
+template <class S, int L, class ROW, bool NT = false>
 struct Along {
   ROW row;
   int row_bytes, chunk;  // chunk: byte offset in a step of what this lane fetches
@@ -196,8 +198,8 @@ struct Along {
     uint32_t place[L];
 #pragma unroll
     for (int u = 0; u < L; ++u) place[u] = first + row(u * S::kLoadRows) * row_bytes;
-    load_lds16<S::kThreads * 16>(resource(o.base + at, max(o.extent - at, 0)),
-                                 to + group_wave<S>() * kWave * 16, place);
+    load_lds16<S::kThreads * 16, NT>(resource(o.base + at, max(o.extent - at, 0)),
+                                     to + group_wave<S>() * kWave * 16, place);
   }
 };
 struct SameRow {

@@ -20,13 +20,13 @@
 //     below 2 (2^-9 .. 1.875) through another: with the weights' codes (1/2 .. 6) every product is
 //     a multiple of 2^(E-13), and nothing is cut.
 //
-// Scales go to LDS like the operands, but 16 bytes of a row at a time: every lane of such a load
-// touches a line of its own, and it is these requests, not the bytes, that cost (a 4-byte word a
-// lane each step: as many requests as the operands' own, and 1790 us for 1285 without
-// them; 256 experts of 256 rows, K = 7168, F = 2048).  A piece is two steps of a row (of an
-// FP8 row: four blocks' fp32 scales).  Where scale rows are no whole words (K % 128 != 0: ODD)
-// a piece is the words that one step's 8 bytes touch.  A scale past its row's end must not be the
-// next row's, which may be NaN: it is cleared after the read (2^-127, times zero codes).
+// Scales go to LDS like the operands, but two steps of a row at a time, 16 bytes (of an FP8 row: four
+// blocks' fp32 scales): such a load touches a line for every row, and it is these requests, not
+// the bytes, that cost (a 4-byte word a lane each step: as many requests as the operands' own,
+// and 1790 us for 1285 without them; 256 experts of 256 rows, K = 7168, F = 2048).  Where scale
+// rows are no whole words (K % 128 != 0: ODD) a piece is 32 bytes from the word on that
+// holds its first byte.  A scale past its row's end must not be the next row's, which may be
+// NaN: it is cleared after the read (2^-127, times zero codes).
 #pragma once
 
 #include "expert_tile.hpp"
@@ -35,10 +35,11 @@ namespace moe {
 namespace tile {
 
 // As Shape.  FP8: the rows are FP8 (the weights are always MX-FP4).
-template <int BI_, int BJ_, int WI_, int WJ_, int NST_, bool FP8_, bool ODD_, int WK_ = 1>
+// NT: the weights pass the caches.
+template <int BI_, int BJ_, int WI_, int WJ_, int NST_, bool FP8_, bool ODD_, bool NT_, int WK_ = 1>
 struct MxShape {
   static constexpr int BI = BI_, BJ = BJ_, WI = WI_, WJ = WJ_, NST = NST_, WK = WK_;
-  static constexpr bool FP8 = FP8_, ODD = ODD_;
+  static constexpr bool FP8 = FP8_, ODD = ODD_, NT = NT_;
   static constexpr int kThreads = WI * WJ * kWave;
   static constexpr int FI = BI / WI / 16, FJ = BJ / WJ / 16;
   static constexpr int loads(int b) { return (b * 8 + kThreads - 1) / kThreads; }
@@ -46,18 +47,29 @@ struct MxShape {
   static constexpr int kLoadRows = kThreads / 8;
   static constexpr int kBytesPart = LI * kThreads * 16;  // of I: 128 bytes of each row
   static constexpr int kBytesI = kParts * kBytesPart, kBytesJ = LJ * kThreads * 16;
-  // pieces of scales: 64 rows a load, of I, then of J, dealt to the waves
-  static constexpr int kWaves = WI * WJ, kGroupsI = (BI + 63) / 64, kGroups = kGroupsI + (BJ + 63) / 64;
-  static constexpr int kSpan = ODD ? 1 : 2;           // steps of a piece
-  // that NST steps in a row can lie in: a tile's last step may have one to itself
-  static constexpr int kPieces = ODD ? NST : NST / 2 + 1 + NST % 2;
+  // pieces of scales: kPieceRows rows a load, of I, then of J, dealt to the waves
+  static constexpr int kWaves = WI * WJ;
+  static constexpr int kSpan = 2, kRowBytes = ODD ? 32 : 16, kPieceRows = 1024 / kRowBytes;
+  static constexpr int kGroupsI = (BI + kPieceRows - 1) / kPieceRows;
+  static constexpr int kGroups = kGroupsI + (BJ + kPieceRows - 1) / kPieceRows;
+  // pieces that NST steps in a row can lie in.  Of one tile, or of one whose pieces are all
+  // whole (a group's are): as many as an unaligned run.  Across a tile's end, x of them before it: its last
+  // piece may be one step.
+  static constexpr int pieces() {
+    int most = (NST + kSpan - 2) / kSpan + 1;
+    for (int x = 1; x < NST && WK == 1; ++x) {
+      const int n = 1 + (x - 1 + kSpan - 1) / kSpan + (NST - x + kSpan - 1) / kSpan;
+      most = n > most ? n : most;
+    }
+    return most;
+  }
+  static constexpr int kPieces = pieces();
   static constexpr int kPieceBytes = kGroups * 1024;
   static constexpr int kStage = kBytesI + kBytesJ;
   static constexpr int kLoadLds = NST * kStage + kPieces * kPieceBytes;
-  static constexpr int kWaveCols = BJ / WJ;
-  static constexpr int kTurnCols = WK == 1 && kWaveCols > 32 ? 32 : kWaveCols;
-  static constexpr int kGroupLds = kLoadLds + WI * WJ * 16 * kTurnCols * 4;
-  static constexpr int kLdsBytes = WK * kGroupLds;
+  // the groups but the first leave their sums behind that
+  static constexpr int kGroupLds = kLoadLds, kSums = FI * FJ * kWave * 16;
+  static constexpr int kLdsBytes = WK * kGroupLds + (WK - 1) * kSums;
   static constexpr int kByLds = 160 * 1024 / kLdsBytes, kByWaves = 8 / (WI * WJ * WK);
   static constexpr int kResident = kByLds < kByWaves ? kByLds : kByWaves;
   static constexpr int kWavesPerSimd = kResident * WI * WJ * WK >= 8 ? 2 : 1;
@@ -77,24 +89,6 @@ struct ScaleRows {
   int bytes;
 };
 
-// A launch's lanes for the scales: 64 tile rows, from row `first` on; ROW as in Along.
-template <class S, class ROW>
-struct PieceLanes {
-  ROW row;
-  int row_bytes;
-  __device__ __forceinline__ void init(int bytes) { row_bytes = bytes; }
-  // the 16 bytes from byte `at` of each row on
-  __device__ __forceinline__ void issue(lds_ptr to, const ScaleRows &s, int first, int rows, int at) const {
-    // whole words from the one on that holds the first byte
-    const int skip = S::ODD ? static_cast<int>(reinterpret_cast<uintptr_t>(s.base) & 3) : 0;
-    const auto r = resource(s.base - skip + at, s.bytes == 0 ? 0 : max(((s.bytes + skip + 3) & ~3) - at, 0));
-    const int tr = first + lane_id(), start = static_cast<int>(row(tr)) * row_bytes + skip;
-    const int word = S::ODD ? start & ~3 : start;
-    const uint32_t place[1] = {tr < rows && word + at < start + row_bytes ? static_cast<uint32_t>(word) : kNowhere};
-    load_lds16<0>(r, to, place);
-  }
-};
-
 struct MxSource {
   Operand i, j;
   ScaleRows x, w;
@@ -110,6 +104,55 @@ __device__ __forceinline__ MxSource either(bool c, const MxSource &a, const MxSo
   return s;
 }
 
+// A launch's lanes for the scales: a wave takes kPieceRows tile rows a load, kRowBytes of each;
+// ROW (of the weights) as in Along.
+template <class S, class ROW>
+struct PieceLanes {
+  static constexpr int kLoads = (S::kGroups + S::kWaves - 1) / S::kWaves;
+  static constexpr int kLanes = S::kRowBytes / 16;  // of a row
+  uint32_t off[kLoads];
+  int x_bytes, w_bytes;  // of a row
+  __device__ __forceinline__ void init(int x, int w, ROW row) {
+    x_bytes = x;
+    w_bytes = w;
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int g = u * S::kWaves + group_wave<S>(), in = lane_id() / kLanes;
+      if (g < S::kGroupsI) {
+        const int r = g * S::kPieceRows + in;
+        off[u] = r < S::BI ? r * x : kNowhere;
+      } else {
+        const int r = (g - S::kGroupsI) * S::kPieceRows + in;
+        off[u] = r < S::BJ ? row(r) * w : kNowhere;
+      }
+    }
+  }
+  // from byte `at` of each row on
+  __device__ __forceinline__ void issue(lds_ptr to, const MxSource &src, int at) const {
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int g = u * S::kWaves + group_wave<S>();
+      if (S::kGroups % S::kWaves != 0 && g >= S::kGroups) return;
+      const bool rows = g < S::kGroupsI;
+      const char *base = rows ? src.x.base : src.w.base;
+      const int bytes = rows ? src.x.bytes : src.w.bytes, row_bytes = rows ? x_bytes : w_bytes;
+      uint32_t place[1];
+      if constexpr (S::ODD) {
+        // whole words from the one on that holds the first byte
+        const int skip = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 3);
+        const uint32_t start = off[u] + skip, word = (start & ~3u) + lane_id() % kLanes * 16;
+        place[0] = word + at < start + row_bytes ? word : kNowhere;
+        load_lds16<0>(resource(base - skip + at, bytes == 0 ? 0 : max(((bytes + skip + 3) & ~3) - at, 0)),
+                      to + g * 1024, place);
+      } else {
+        const int in_row = lane_id() % kLanes * 16;
+        place[0] = in_row + at < row_bytes ? off[u] + in_row : kNowhere;
+        load_lds16<0>(resource(base + at, max(bytes - at, 0)), to + g * 1024, place);
+      }
+    }
+  }
+};
+
 // Where a workgroup stands in the ring of pieces.
 struct Ring {
   int at = 0;
@@ -122,28 +165,18 @@ struct Ring {
 template <class S, class ROW>
 struct MxFeed {
   Along<S, S::LI, SameRow> i;
-  Along<S, S::LJ, ROW> j;
-  PieceLanes<S, SameRow> x;
-  PieceLanes<S, ROW> w;
+  Along<S, S::LJ, ROW, S::NT> j;
+  PieceLanes<S, ROW> s;
   // step of the contraction that a group takes as its step-th
   __device__ __forceinline__ int global_step(int step) const {
     if constexpr (S::WK == 1) return step;
-    if constexpr (S::ODD) return step * S::WK + group_id<S>();
-    return (step / 2 * S::WK + group_id<S>()) * 2 + step % 2;  // (pieces stay whole)
+    return (step / S::kSpan * S::WK + group_id<S>()) * S::kSpan + step % S::kSpan;  // (pieces stay whole)
   }
   __device__ __forceinline__ void issue(lds_ptr lds, int stage, Ring &piece, const MxSource &src, int step) const {
     const int t = global_step(step);
     if (step % S::kSpan == 0) {
-      lds_ptr to = lds + S::NST * S::kStage + piece.at * S::kPieceBytes;
+      s.issue(lds + S::NST * S::kStage + piece.at * S::kPieceBytes, src, t * 8);
       piece.template advance<S::kPieces>();
-#pragma unroll
-      for (int u = 0; u < (S::kGroups + S::kWaves - 1) / S::kWaves; ++u) {
-        const int g = u * S::kWaves + group_wave<S>();
-        if (g < S::kGroupsI)
-          x.issue(to + g * 1024, src.x, g * 64, S::BI, t * 8);
-        else if (g < S::kGroups)
-          w.issue(to + g * 1024, src.w, (g - S::kGroupsI) * 64, S::BJ, t * 8);
-      }
     }
     lds_ptr to = lds + stage * S::kStage;
 #pragma unroll
@@ -180,7 +213,7 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
   const int at_i = row_i * kStepBytes + ((chunk ^ (r & 7)) * 16);
   const int at_j = row_j * kStepBytes + ((chunk ^ (r & 7)) * 16);
   // and, in a piece, of their scales
-  int scale_i = row_i * 16, scale_j = S::kGroupsI * 1024 + row_j * 16;
+  int scale_i = row_i * S::kRowBytes, scale_j = S::kGroupsI * 1024 + row_j * S::kRowBytes;
   if constexpr (S::FP8) {
     scale_j += q;
   } else if constexpr (S::ODD) {
@@ -196,7 +229,9 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
 #pragma unroll
     for (int b = 0; b < S::FJ; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  const int steps = max(cur.steps, S::NST);
+  // (a shorter tile goes through NST steps all the same, of zeros; a group's are whole pieces)
+  constexpr int kLeast = S::WK > 1 ? (S::NST + S::kSpan - 1) / S::kSpan * S::kSpan : S::NST;
+  const int steps = max(cur.steps, kLeast);
   int stage = at.stage;
   lds_ptr pieces = lds + S::NST * S::kStage, scales = pieces + at.read.at * S::kPieceBytes;
   auto turn_over = [&](int t) {
@@ -244,20 +279,20 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
       lds_ptr p = ti + half * S::kBytesPart + block * kStepBytes;
       vi[set] = __builtin_shufflevector(*(MOE_LDS const i32x4 *)(p + at_i), *(MOE_LDS const i32x4 *)(p + (at_i ^ 64)),
                                         0, 1, 2, 3, 4, 5, 6, 7);
-      fi[set] = __builtin_bit_cast(float, *(MOE_LDS const int *)(scales + scale_i + half * 4 + block * 16) & mask[half]);
+      fi[set] = __builtin_bit_cast(float, *(MOE_LDS const int *)(scales + scale_i + half * 4 + block * S::kRowBytes) & mask[half]);
     } else {
       const i32x4 v = *(MOE_LDS const i32x4 *)(ti + (half ? at_i ^ swap : at_i) + block * kStepBytes);
       vi[set] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-      if (half == 0) si[blk] = short_at(scales + scale_i + block * 16);
+      if (half == 0) si[blk] = short_at(scales + scale_i + block * S::kRowBytes);
     }
   };
   auto read_j = [&](int b, int half) {
     lds_ptr tj = lds + stage * S::kStage + S::kBytesI;
     vj[b] = *(MOE_LDS const i32x4 *)(tj + (half ? at_j ^ swap : at_j) + b * 16 * kStepBytes);
     if constexpr (S::FP8)
-      sj[b] = *(MOE_LDS const uint8_t *)(scales + scale_j + half * 4 + b * 256) & mask[half];
+      sj[b] = *(MOE_LDS const uint8_t *)(scales + scale_j + half * 4 + b * 16 * S::kRowBytes) & mask[half];
     else if (half == 0)
-      sj[b] = short_at(scales + scale_j + b * 256);
+      sj[b] = short_at(scales + scale_j + b * 16 * S::kRowBytes);
   };
   auto wide = [](i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); };
 

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const uint16_t *x, u
       float v[8];
       unpack8(r4, v);
       uint32_t scale;
-      const uint32_t c = mx_encode8(v, scale);
+      const uint32_t c = mx_encode8(v, quad_max(mx_lane_max(v)), scale);
       if (at < pieces) {
         reinterpret_cast<uint32_t *>(codes)[at] = c;
         if ((threadIdx.x & 3) == 0) scales[at / 4] = static_cast<uint8_t>(scale);

@@ -569,11 +569,11 @@ MOE_API int moe_check_expert_mx_op(const moe_problem *p, const moe_expert_op *op
  * x_scales and w_scales are 4-byte aligned, and readable to the end of the 4-byte
  * word that holds their last byte (K % 128 != 0: scale rows are no whole words).
  *
- * MX-FP4 rows: the scaled matrix instruction multiplies and adds in fp32 (a product is kept to
- * 2^-21 of the largest term that it is added with).  FP8 rows: within a 128-value block the
- * products lose the bits that moe_expert_glu's do, cut relative to w's scaled codes;
- * the blocks' sums are multiplied by x's fp32 scale and added in fp32.  Row
- * ranges, untouched rows, repeatability and NaN: as the experts' products above. */
+ * Products are whole: the scaled matrix instruction keeps every one of MX-FP4 rows, and FP8
+ * rows go through it in two halves, codes of 2 and above and codes below, for the same.  It
+ * adds them up in fp32 (an addition is off by up to 2^-20 of its largest term); the sums of an
+ * FP8 row's blocks are multiplied by its fp32 scale and added in fp32.  Row ranges, untouched
+ * rows, repeatability and NaN: as the experts' products above. */
 MOE_API int moe_expert_glu_mx(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
                               const void *x, const void *x_scales, const uint8_t *w,
                               const uint8_t *w_scales, const float *bias, void *h,

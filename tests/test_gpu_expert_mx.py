@@ -2,11 +2,10 @@
 64-bit references, element by element.  Rows that hold no token are poisoned in every input
 (codes of 6, NaN scales) and must come back untouched in every output.
 
-Bounds: those of the other products (expert_reference.py).  The scaled instruction keeps a
-product to 2^-20 of the largest term that it is added with, of K / 128 additions: less than
-the (K + 8) 2^-23 of the sum of magnitudes that the reference allows from K >= 32 on
-(K / 128 * 2^-20 = K / 16 * 2^-23).  FP8 rows: the products of eight neighbouring columns are
-cut to multiples of 2^(E-13), E the largest sum of the two codes' exponents, scaled."""
+Bounds: those of the other products (expert_reference.py).  An addition of the scaled
+instruction, of 128 products and the sum so far, is off by up to 2^-20 of the largest term: K / 128
+of them (K / 64 of FP8 rows, in two halves) by less than the (K + 8) 2^-23 of the sum of
+magnitudes that the reference allows (2^-20 = 8 * 2^-23, and K / 64 * 8 < K)."""
 import numpy as np
 import pytest
 import torch
@@ -62,24 +61,6 @@ def fp8_rows(r, k):
     codes = (x / scales[..., None]).to(torch.float8_e4m3fn).view(r.rows, k).view(torch.uint8).clone()
     codes[~r.live], scales[~r.live] = 0x7F, float("nan")
     return codes, scales
-
-
-def group_cut(xc, xs, wc, ws):
-    """What the instruction may cut from the sums of FP8 rows with MX-FP4 weights: [rows, n]."""
-    v = xc.view(torch.float8_e4m3fn).float().abs()
-    ex = torch.where(v == 0, -100.0, (torch.frexp(v.clamp(min=2.0 ** -6))[1] - 1).float())
-    t = TABLE.to(wc.device).abs()
-    v = torch.stack([t[(wc & 15).long()], t[(wc >> 4).long()]], -1).reshape(wc.shape[0], -1).float()
-    # the exponent of a code of 1/2 (subnormal) is that of 1
-    ew = torch.where(v == 0, -100.0, (torch.frexp(v.clamp(min=1.0))[1] - 1).float())
-    ew = ew + (ws.float() - 127).repeat_interleave(32, -1)
-    rows, n, k = xc.shape[0], wc.shape[0], xc.shape[1]
-    out = torch.empty(rows, n, dtype=torch.float64, device=xc.device)
-    for i in range(rows):
-        top = (ex[i] + ew).view(n, k // 8, 8).amax(-1)
-        cut = 7 * torch.exp2(top.double() - 13)
-        out[i] = (cut.view(n, k // 128, 16).sum(-1) * xs[i].double()).sum(-1)
-    return out
 
 
 def check_quantised(codes, scales, y, dy, what):
@@ -175,21 +156,34 @@ def test_forward(moe, i, glu, fmt):
         X = mx_value(x[a:b], xs[a:b]) if fmt == "mxfp4" else ref.dequant_rows(x[a:b], xs[a:b])
         _, ry, _, ty = ref.forward(X, mx_value(w[e], ws[e]), None if bias is None else bias[e].double(), glu, name,
                                    None if residual is None else residual[a:b].double())
-        if fmt == "fp8":
-            b = min(b, a + 40)  # (memory of the groups' maxima)
-            ry, ty = ry[: b - a], ty[: b - a]
-            cut = group_cut(x[a:b], xs[a:b], w[e], ws[e])
-            z = X[: b - a] @ mx_value(w[e], ws[e]).T + (0 if bias is None else bias[e].double())
-            if glu:
-                ag = ref.act(z[:, :f], name)
-                da = 1.13 * cut[:, :f]
-                more = da * z[:, f:].abs() + ag.abs() * cut[:, f:] + da * cut[:, f:]
-            else:
-                more = 1.13 * cut
-            ty = ty + more * (1 + ref.BF16)
         assert_within(y[a:b], ry, ty, f"y of expert {e}")
         if q is not None:
             check_quantised(q[a:b], qs[a:b], ry, ty, f"h of expert {e}")
+
+
+@pytest.mark.parametrize("c", [dict(tokens=6, experts=3, k=256, f=128), dict(tokens=90, experts=2, k=384, f=256),
+                               dict(tokens=400, experts=16, k=1536, f=520), dict(tokens=900, experts=2, k=128, f=2048),
+                               dict(tokens=12, experts=2, k=2176, f=128)])
+def test_fp8_rows_of_any_code(moe, c):
+    """Codes from 2^-9 to 448 beside each other: no product is cut, in any tile."""
+    say(f"[expert mx] any code {c}")
+    r = Routed(moe, 500 + c["k"], c["tokens"], c["experts"], 1)
+    k, f = c["k"], c["f"]
+    x = torch.randint(0, 256, (r.rows, k), generator=r.g, device="cuda", dtype=torch.int32).to(torch.uint8)
+    x = torch.where((x & 0x7F) == 0x7F, torch.zeros_like(x), x)
+    xs = 0.5 + torch.rand(r.rows, k // 128, generator=r.g, device="cuda")
+    w = torch.randint(0, 256, (r.experts, f, k // 2), generator=r.g, device="cuda", dtype=torch.int32).to(torch.uint8)
+    ws = torch.randint(110, 118, (r.experts, f, k // 32), generator=r.g, device="cuda").to(torch.uint8)
+    y, rest, op = r.sentinel(f), r.sentinel(f), moe.expert_op(k, f, fmt="fp8")
+    moe.moe_expert_linear_mx(r.p, r.plan, op, x, xs, w, ws, y)
+    # with -y for the residual: what the rounding took off, so that the sum itself is seen
+    moe.moe_expert_linear_mx(r.p, r.plan, op, x, xs, w, ws, rest, residual=-y)
+    for e, (a, b) in enumerate(r.ranges):
+        X, W = ref.dequant_rows(x[a:b], xs[a:b]), mx_value(w[e], ws[e])
+        z, tol = X @ W.T, (k + 8) * ref.F32 * (X.abs() @ W.abs().T)
+        assert_within(y[a:b], z, tol + ref.BF16 * (z.abs() + tol), f"y of expert {e}")
+        left = z - y[a:b].double()
+        assert_within(rest[a:b], left, tol + ref.F32 * z.abs() + ref.BF16 * (left.abs() + tol), f"rest of expert {e}")
 
 
 def test_exact_sums(moe):
