@@ -452,13 +452,11 @@ def moe_combine(p: Problem, plan: PlanBuffers, expert_out: torch.Tensor,
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _own_stream(stream, plan: PlanBuffers | None, *tensors) -> int:
+def _own_stream(stream, plan: PlanBuffers, *tensors) -> int:
     """The raw stream to launch on; the kernels run on the current device, so every
     buffer must live there."""
     here = _current_device()
-    if plan is not None:
-        tensors += (plan.slot, plan.expert_counts, plan.expert_offsets)
-    for t in tensors:
+    for t in (plan.slot, plan.expert_counts, plan.expert_offsets, *tensors):
         if t is not None and t.get_device() != here:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
     if stream is not None:
@@ -592,18 +590,46 @@ def moe_expert_linear_backward(p: Problem, plan: PlanBuffers, op: ExpertOp, dy: 
                      preact, x, w, dz, dx, dw, dbias, workspace, stream)
 
 
+class _Call:
+    """What a call's tensors are held to: on the current device, contiguous, of one of the
+    types, large enough.  (One look at each; what is wrong is found out where something is.)"""
+    __slots__ = ("here",)
+
+    def __init__(self):
+        try:
+            self.here = _current_device()
+        except RuntimeError:  # no device at all: every tensor is refused as a host tensor
+            self.here = -2
+
+    def __call__(self, t: torch.Tensor | None, name: str, dtypes, numel: int):
+        if t is None:
+            return None
+        if t.get_device() == self.here and t.dtype in dtypes and t.numel() >= numel and t.is_contiguous():
+            return t.data_ptr()
+        _dev(t, name, dtypes, numel)
+        raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{self.here}")
+
+    def stream(self, stream) -> int:
+        if stream is not None:
+            return stream.cuda_stream
+        return _raw_stream(self.here) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+_I32, _F32, _U8 = (torch.int32,), (torch.float32,), (torch.uint8,)
+_FP8 = (torch.uint8, torch.float8_e4m3fn)
+
+
 # ---- MX-FP4: quantisation, and the experts' products with MX-FP4 weights -----------
 
 def moe_quantize_mxfp4(x: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, stream=None) -> None:
     """bf16 [..., C] -> MX-FP4 codes uint8 [..., C/2] and scale bytes [..., C/32]."""
     if x.dim() == 0:
         raise ValueError("x needs a last dimension of whole 32-value blocks")
-    cols = x.shape[-1]
-    rows = x.numel() // cols if cols else 0
-    args = (_dev(x, "x", _BF16), _dev(codes, "codes", (torch.uint8,), rows * (cols // 2)),
-            _dev(scales, "scales", (torch.uint8,), rows * (cols // 32)))
-    raw = _own_stream(stream, None, x, codes, scales)
-    _checked(lib.moe_quantize_mxfp4(rows, cols, *args, raw), "moe_quantize_mxfp4")
+    n, cols = x.numel(), x.shape[-1]
+    arg = _Call()
+    args = (arg(x, "x", _BF16, n), arg(codes, "codes", _U8, n // 2), arg(scales, "scales", _U8, n // 32))
+    _checked(lib.moe_quantize_mxfp4(n // cols if cols else 0, cols, *args, arg.stream(stream)),
+             "moe_quantize_mxfp4")
 
 
 def moe_check_expert_mx_op(p: Problem, op: ExpertOp) -> int:
@@ -611,18 +637,18 @@ def moe_check_expert_mx_op(p: Problem, op: ExpertOp) -> int:
     return int(lib.moe_check_expert_mx_op(ctypes.byref(p), ctypes.byref(op)))
 
 
-def _mx_args(p, plan, op, wide, x, x_scales, w, w_scales, bias):
-    rows, e, k, n = _sizes(p)[0], p.n_experts, op.in_dim, wide * op.out_dim
+def _mx_args(arg, rows, p, plan, op, wide, x, x_scales, w, w_scales, bias):
+    e, k = p.n_experts, op.in_dim
+    n = e * wide * op.out_dim
+    arg(plan.expert_counts, "plan.expert_counts", _I32, e)
+    arg(plan.expert_offsets, "plan.expert_offsets", _I32, e + 1)
     if op.fmt == FMT["fp8"]:
-        args = [_dev(x, "x", (torch.uint8, torch.float8_e4m3fn), rows * k),
-                _dev(x_scales, "x_scales", (torch.float32,), rows * (k // 128))]
+        rows_of = (arg(x, "x", _FP8, rows * k), arg(x_scales, "x_scales", _F32, rows * (k // 128)))
     else:
-        args = [_dev(x, "x", (torch.uint8,), rows * (k // 2)),
-                _dev(x_scales, "x_scales", (torch.uint8,), rows * (k // 32))]
-    _plan_rows(plan, e)
-    return args + [_dev(w, "w", (torch.uint8,), e * n * (k // 2)),
-                   _dev(w_scales, "w_scales", (torch.uint8,), e * n * (k // 32)),
-                   _dev(bias, "bias", (torch.float32,), e * n) or None]
+        rows_of = (arg(x, "x", _U8, rows * (k // 2)), arg(x_scales, "x_scales", _U8, rows * (k // 32)))
+    return (ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *rows_of,
+            arg(w, "w", _U8, n * (k // 2)), arg(w_scales, "w_scales", _U8, n * (k // 32)),
+            arg(bias, "bias", _F32, n))
 
 
 def moe_expert_glu_mx(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor, x_scales: torch.Tensor,
@@ -631,16 +657,13 @@ def moe_expert_glu_mx(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tens
                       stream=None) -> None:
     """moe_expert_glu with MX-FP4 weights (w uint8 [E, 2F, K/2], w_scales [E, 2F, K/32]) and
     rows of op.fmt; h bf16 [R_max, F], or with h_scales MX-FP4 codes [R_max, F/2]."""
-    args = _mx_args(p, plan, op, 2, x, x_scales, w, w_scales, bias)
-    rows, n = _sizes(p)[0], op.out_dim
+    arg, rows, n = _Call(), _sizes(p)[0], op.out_dim
+    args = _mx_args(arg, rows, p, plan, op, 2, x, x_scales, w, w_scales, bias)
     if h_scales is None:
-        out = [_dev(h, "h", _BF16, rows * n), None]
+        out = (arg(h, "h", _BF16, rows * n), None)
     else:
-        out = [_dev(h, "h", (torch.uint8,), rows * (n // 2)),
-               _dev(h_scales, "h_scales", (torch.uint8,), rows * (n // 32))]
-    raw = _own_stream(stream, plan, x, x_scales, w, w_scales, bias, h, h_scales)
-    _checked(lib.moe_expert_glu_mx(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op), *args,
-                                   *out, raw), "moe_expert_glu_mx")
+        out = (arg(h, "h", _U8, rows * (n // 2)), arg(h_scales, "h_scales", _U8, rows * (n // 32)))
+    _checked(lib.moe_expert_glu_mx(*args, *out, arg.stream(stream)), "moe_expert_glu_mx")
 
 
 def moe_expert_linear_mx(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.Tensor,
@@ -649,12 +672,11 @@ def moe_expert_linear_mx(p: Problem, plan: PlanBuffers, op: ExpertOp, x: torch.T
                          stream=None) -> None:
     """moe_expert_linear with MX-FP4 weights (w uint8 [E, F, K/2], w_scales [E, F, K/32]) and
     rows of op.fmt; y and residual bf16 [R_max, F]."""
-    args = _mx_args(p, plan, op, 1, x, x_scales, w, w_scales, bias)
-    n = _sizes(p)[0] * op.out_dim
-    args += [_dev(residual, "residual", _BF16, n) or None, _dev(y, "y", _BF16, n)]
-    raw = _own_stream(stream, plan, x, x_scales, w, w_scales, bias, residual, y)
-    _checked(lib.moe_expert_linear_mx(ctypes.byref(p), ctypes.byref(plan.as_struct()), ctypes.byref(op),
-                                      *args, raw), "moe_expert_linear_mx")
+    arg, rows = _Call(), _sizes(p)[0]
+    n = rows * op.out_dim
+    args = _mx_args(arg, rows, p, plan, op, 1, x, x_scales, w, w_scales, bias)
+    _checked(lib.moe_expert_linear_mx(*args, arg(residual, "residual", _BF16, n), arg(y, "y", _BF16, n),
+                                      arg.stream(stream)), "moe_expert_linear_mx")
 
 
 # ---- routing: scores, top-k experts, gate weights ----------------------------------
@@ -669,35 +691,29 @@ def moe_check_router(p: Problem, r: Router) -> int:
     return int(lib.moe_check_router(ctypes.byref(p), ctypes.byref(r)))
 
 
-def _logits(r: Router):
-    return (torch.float32,) if r.logits == LOGITS["fp32"] else _BF16
-
-
 def moe_route(p: Problem, r: Router, logits: torch.Tensor, topk_ids: torch.Tensor,
               topk_weights: torch.Tensor | None, bias: torch.Tensor | None = None,
               scores: torch.Tensor | None = None, stream=None) -> None:
     """Top-k experts of every token (topk_ids int32 [N, k], -1 where none is left) and their gate
     weights (float [N, k], or None) from logits [N, E]; scores: float [N, E] or None."""
-    nk, ne = p.n_tokens * p.top_k, p.n_tokens * p.n_experts
-    args = (_dev(logits, "logits", _logits(r), ne), _dev(bias, "bias", (torch.float32,), p.n_experts) or None,
-            _dev(topk_ids, "topk_ids", (torch.int32,), nk),
-            _dev(topk_weights, "topk_weights", (torch.float32,), nk) or None,
-            _dev(scores, "scores", (torch.float32,), ne) or None)
-    raw = _own_stream(stream, None, logits, bias, topk_ids, topk_weights, scores)
-    _checked(lib.moe_route(ctypes.byref(p), ctypes.byref(r), *args, raw), "moe_route")
+    n, e = p.n_tokens, p.n_experts
+    nk, ne, arg = n * p.top_k, n * e, _Call()
+    _checked(lib.moe_route(ctypes.byref(p), ctypes.byref(r),
+                           arg(logits, "logits", _BF16 if r.logits else _F32, ne), arg(bias, "bias", _F32, e),
+                           arg(topk_ids, "topk_ids", _I32, nk), arg(topk_weights, "topk_weights", _F32, nk),
+                           arg(scores, "scores", _F32, ne), arg.stream(stream)), "moe_route")
 
 
 def moe_route_backward(p: Problem, r: Router, logits: torch.Tensor, topk_ids: torch.Tensor | None,
                        dlogits: torch.Tensor, dweights: torch.Tensor | None = None,
                        dscores: torch.Tensor | None = None, stream=None) -> None:
     """dlogits [N, E] from the gradients of moe_route's weights [N, k] and scores [N, E]."""
-    nk, ne = p.n_tokens * p.top_k, p.n_tokens * p.n_experts
-    args = (_dev(logits, "logits", _logits(r), ne), _dev(topk_ids, "topk_ids", (torch.int32,), nk) or None,
-            _dev(dweights, "dweights", (torch.float32,), nk) or None,
-            _dev(dscores, "dscores", (torch.float32,), ne) or None,
-            _dev(dlogits, "dlogits", _logits(r), ne))
-    raw = _own_stream(stream, None, logits, topk_ids, dlogits, dweights, dscores)
-    _checked(lib.moe_route_backward(ctypes.byref(p), ctypes.byref(r), *args, raw), "moe_route_backward")
+    nk, ne, arg = p.n_tokens * p.top_k, p.n_tokens * p.n_experts, _Call()
+    kind = _BF16 if r.logits else _F32
+    _checked(lib.moe_route_backward(ctypes.byref(p), ctypes.byref(r), arg(logits, "logits", kind, ne),
+                                    arg(topk_ids, "topk_ids", _I32, nk), arg(dweights, "dweights", _F32, nk),
+                                    arg(dscores, "dscores", _F32, ne), arg(dlogits, "dlogits", kind, ne),
+                                    arg.stream(stream)), "moe_route_backward")
 
 
 # ---- exchange across EP simulated ranks ---------------------------------------
