@@ -213,13 +213,17 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
   const int at_i = row_i * kStepBytes + ((chunk ^ (r & 7)) * 16);
   const int at_j = row_j * kStepBytes + ((chunk ^ (r & 7)) * 16);
   // and, in a piece, of their scales
-  int scale_i = row_i * S::kRowBytes, scale_j = S::kGroupsI * 1024 + row_j * S::kRowBytes;
+  int word_i = 0, word_j = 0, scale_i = row_i * S::kRowBytes, scale_j = S::kGroupsI * 1024 + row_j * S::kRowBytes;
   if constexpr (S::FP8) {
     scale_j += q;
   } else if constexpr (S::ODD) {
     // (16 rows on, and an even number of gate rows on, a row starts at the same place in a word)
     scale_i += ((r * blocks + static_cast<int>(reinterpret_cast<uintptr_t>(cur.x.base) & 3)) & 3) + 2 * q;
     scale_j += ((r * blocks + static_cast<int>(reinterpret_cast<uintptr_t>(cur.w.base) & 3)) & 3) + 2 * q;
+    word_i = scale_i & 3;
+    word_j = scale_j & 3;
+    scale_i -= word_i;
+    scale_j -= word_j;
   } else {
     scale_i += 2 * q;
     scale_j += 2 * q;
@@ -256,12 +260,14 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
   // scale bytes of the step that si and sj belong to that lie in the row (a piece past the
   // row's end holds the next row's)
   int mask[S::FP8 ? 2 : 1];
-  typedef uint16_t __attribute__((aligned(1), may_alias)) loose16;
-  auto short_at = [&](lds_ptr p) -> int {
-    if constexpr (S::ODD)
-      return *(MOE_LDS const loose16 *)p & mask[0];
-    else
-      return *(MOE_LDS const uint16_t *)p & mask[0];
+  // two scale bytes from `at` on; ODD: anywhere in a word, whose place in it is `in_word`
+  auto short_at = [&](lds_ptr at, int in_word) -> int {
+    if constexpr (S::ODD) {
+      MOE_LDS const uint32_t *p = (MOE_LDS const uint32_t *)at;
+      return static_cast<int>(__builtin_amdgcn_alignbyte(p[1], p[0], in_word)) & mask[0];
+    } else {
+      return *(MOE_LDS const uint16_t *)at & mask[0];
+    }
   };
   auto set_mask = [&](int t) {
     const int left = blocks - feed.global_step(t) * 8;
@@ -283,7 +289,7 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
     } else {
       const i32x4 v = *(MOE_LDS const i32x4 *)(ti + (half ? at_i ^ swap : at_i) + block * kStepBytes);
       vi[set] = __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1);
-      if (half == 0) si[blk] = short_at(scales + scale_i + block * S::kRowBytes);
+      if (half == 0) si[blk] = short_at(scales + scale_i + block * S::kRowBytes, word_i);
     }
   };
   auto read_j = [&](int b, int half) {
@@ -292,7 +298,7 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
     if constexpr (S::FP8)
       sj[b] = *(MOE_LDS const uint8_t *)(scales + scale_j + half * 4 + b * 16 * S::kRowBytes) & mask[half];
     else if (half == 0)
-      sj[b] = short_at(scales + scale_j + b * 16 * S::kRowBytes);
+      sj[b] = short_at(scales + scale_j + b * 16 * S::kRowBytes, word_j);
   };
   auto wide = [](i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); };
 
