@@ -232,7 +232,7 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 //   FP8: 16 x 64, K in four 11.2   909.6           92.7         145.6^        690.9
 //        16 x 64            20.2   640.2           78.7         110.7^        520.2
 //        64 x 128           27.6   887.5           69.6          72.7^        225.2
-//        128 x 256          54.1  1406.3          109.8         110.4^        213.0
+//        128 x 256          54.1  1406.3          109.8         110.4^        208.4
 // (* K = 7168, F = 2048, 256 experts; ** linear, K = 2048, N = 4096; *** F = 2048; ^ 32 rows; 96: 133.8
 // of 64 x 128, 114.4 of 128 x 256.)
 // A tile of 16 rows is one wave with two stages, so that a compute unit holds six and the
@@ -243,7 +243,7 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 // x 128 and 256 x 256: K = 512 59.7 / 61.8, 1024 81.9 / 81.7, 2048 131.0 / 125.8; linear, N = 7168, K = 1024
 // 84.6 / 90.6), nor does one whose rows (K / 2 bytes) start inside a line: of each the two lines
 // that a step touches come twice, more often than the caches keep them (256 rows, N = 4096,
-// K = 4128 471 / 549).
+// K = 4128 313 / 579).
 template <bool GLU, bool FP8, bool ODD>
 hipError_t launch_sized(const MxArgs &g, int64_t pairs, hipStream_t stream) {
   typedef MxShape<16, 64, 1, 1, FP8 ? 2 : 3, FP8, ODD, true, 4> Split;
