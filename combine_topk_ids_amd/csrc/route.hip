@@ -30,6 +30,14 @@ __device__ __forceinline__ V pick(bool c, V a, V b) {
   return c ? a : b;
 }
 
+// What the wave's lanes wrote to LDS before is what they read after.  (LDS serves a wave in order;
+// this keeps the compiler to it: no instruction.)
+__device__ __forceinline__ void lanes_meet() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+}
+
 // -------------------------------------------------- a token's lanes ---
 
 // f(v of a lane, v of its partner) over the L lanes of a token, in a fixed order: every
@@ -279,8 +287,8 @@ __device__ __forceinline__ double key_value(uint64_t u) {
 // A sigmoid is off by at most 4.2 * 2^-24 (exp_fine's error and that of its argument weigh s (1 - s),
 // the sum and the reciprocal 1.5 * 2^-23 s), four of them by 2^-19.  A softmax score is off by at
 // most 27 * 2^-24 of itself (a sum of 1024 terms, 16 in a lane), and scores of a row add up to 1
-// at most: two sets of them by 2^-18.  (A NaN or two infinities are not near: neither becomes
-// another value in 64 bits.)
+// at most: two sets of them by 2^-18.  (A NaN or two infinities are not near: a score with its bias
+// never overflows, so neither becomes another value in 64 bits.)
 constexpr float kSigmoidSlack = 0x1p-19f, kSoftmaxSlack = 0x1p-18f;
 __device__ __forceinline__ bool too_near(float a, float b, float slack) {
   return a - b <= slack + 0x1p-21f * fabsf(a);
@@ -413,9 +421,19 @@ __device__ __forceinline__ int choose_short(const uint32_t (&key)[PER], int k) {
   return lane < k && mine != 0 ? static_cast<int>(0xFFFFu - (mine & 0xFFFFu)) : -1;
 }
 
-// A group's key from its two best (0: none): the best, or with `two` the sum's.
-template <class K>
-__device__ __forceinline__ K group_key(K first, K second, bool two) {
+// A group's key from its two best (0: none): the best, or with `two` the sum's.  error: what the
+// roundings of two biased scores and of their sum, each by 2^-24, and of adding this to it come to:
+// the two can cancel, so it goes by them and not by the sum.
+__device__ __forceinline__ uint32_t group_key(uint32_t first, uint32_t second, bool two, float &error) {
+  const float a = key_value(first);
+  error = first != 0 ? 0x1p-22f * fabsf(a) : 0.0f;
+  if (!two || second == 0) return first;
+  const float b = key_value(second), sum = a + b;
+  error += 0x1p-22f * fabsf(b);
+  // (a sum below all numbers is still one that can be chosen)
+  return order_key(pick(sum == -kInf, -__FLT_MAX__, sum));
+}
+__device__ __forceinline__ uint64_t group_key(uint64_t first, uint64_t second, bool two, float &) {
   return two && second != 0 ? order_key(key_value(first) + key_value(second)) : first;
 }
 
@@ -426,14 +444,19 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &g, const V (&value)
                                             K (&key)[PER], float slack, bool &near) {
   const int lane = lane_id() & (L - 1), e0 = lane * PER;
   const bool two = g.group_top == 2;
-  // of the lane's own groups: the lowest key kept, the highest left out
+  // of the lane's own groups: the lowest that a kept one can be, the highest of one left out
+  // (past the largest number a NaN, which settles nothing below)
   V kept = static_cast<V>(~0ull), out = 0;
-  auto place = [&](V mine, int better) {
-    if (better < g.top_groups)
-      kept = mine < kept ? mine : kept;
-    else
-      out = mine > out ? mine : out;
-    return better < g.top_groups;
+  auto place = [&](V mine, float error, int better) {
+    const bool keep = better < g.top_groups;
+    if constexpr (NEAR) {
+      const V at = mine == 0 ? 0 : order_key(key_value(mine) + (keep ? -error : error));
+      if (keep)
+        kept = at < kept ? at : kept;
+      else
+        out = at > out ? at : out;
+    }
+    return keep;
   };
   // lanes that hold a group, where it is a power of two of them
   const int group_lanes = g.group_size % PER ? 0 : g.group_size / PER;
@@ -459,24 +482,25 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &g, const V (&value)
     merge(std::integral_constant<int, 8>());
     if constexpr (L >= 32) merge(std::integral_constant<int, 16>());
     if constexpr (L >= 64) merge(std::integral_constant<int, 32>());
-    const V mine = group_key(first, second, two);
+    float error = 0.0f;
+    const V mine = group_key(first, second, two, error);
     const int own = lane / group_lanes;
     int better = 0;
     for (int h = 0; h < g.groups; ++h) {
       const V u = lane_value<L>(mine, h * group_lanes);
       better += u > mine || (u == mine && h < own);
     }
-    if (own < g.groups && !place(mine, better)) {
+    if (own < g.groups && !place(mine, error, better)) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) key[i] = 0;
     }
   } else {
     V *row = reinterpret_cast<V *>(lds_row);
-    __builtin_amdgcn_wave_barrier();
+    lanes_meet();
 #pragma unroll
     for (int i = 0; i < PER; ++i) row[e0 + i] = value[i];
-    __builtin_amdgcn_wave_barrier();
-    // a group's key takes the place of its first expert's
+    lanes_meet();
+    // a group's key takes the place of its first expert's, the error the next
     for (int q = lane; q < g.groups; q += L) {
       V first = 0, second = 0;
       for (int i = 0; i < g.group_size; ++i) {
@@ -485,9 +509,13 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &g, const V (&value)
         first = u > first ? u : first;
         second = low > second ? low : second;
       }
-      row[q * g.group_size] = group_key(first, second, two);
+      float error = 0.0f;
+      row[q * g.group_size] = group_key(first, second, two, error);
+      if constexpr (NEAR) {
+        if (g.group_size > 1) row[q * g.group_size + 1] = __float_as_uint(error);
+      }
     }
-    __builtin_amdgcn_wave_barrier();
+    lanes_meet();
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int e = e0 + i;
@@ -499,15 +527,19 @@ __device__ __forceinline__ void keep_groups(const RouteArgs &g, const V (&value)
           const V u = row[h * g.group_size];
           better += u > mine || (u == mine && h < q);
         }
-        if (!place(mine, better)) key[i] = 0;
+        float error = 0.0f;
+        if constexpr (NEAR)
+          error = g.group_size > 1 ? __uint_as_float(row[q * g.group_size + 1])
+                                   : 0x1p-22f * fabsf(key_value(mine));
+        if (!place(mine, error, better)) key[i] = 0;
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    lanes_meet();
   }
   if constexpr (NEAR) {
     kept = ~lanes_best<L>(static_cast<V>(~kept));
     out = lanes_best<L>(out);
-    if (out != 0) near = near || too_near(key_value(kept), key_value(out), slack);
+    if (out != 0) near = near || !(key_value(kept) - key_value(out) > slack);
   }
 }
 
@@ -701,14 +733,14 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteGradArgs 
         if (j < lane) first = false;
       }
     }
-    __builtin_amdgcn_wave_barrier();
+    lanes_meet();
     if (first) add[id] = total;
-    __builtin_amdgcn_wave_barrier();
+    lanes_meet();
   }
   float out[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) out[i] = add[e0 + i];
-  __builtin_amdgcn_wave_barrier();
+  lanes_meet();
   if (whole) {
     if (g.sigmoid) {
 #pragma unroll

@@ -376,8 +376,8 @@ MOE_API int moe_combine_backward(const moe_problem *p, const moe_plan *plan,
  * rounding.  An expert whose logit or key is -inf is never chosen (a switched-off
  * expert, a row without a token): where fewer than k are left, the other IDs are -1 with
  * weight 0, which the plan takes as masked.  A row of -inf has scores 0 under softmax.  A NaN
- * key ranks first, and a NaN logit makes its token's softmax scores NaN: it shows in that
- * token's weights and in no other's.  Renormalised softmax weights are the softmax
+ * key ranks first, and a NaN logit (or +inf) makes its token's softmax scores NaN: it shows in
+ * that token's weights and in no other's.  Renormalised softmax weights are the softmax
  * over the chosen logits alone; chosen sigmoid scores that sum to 0 in fp32
  * (logits below -87) give weights 0.
  *
@@ -406,7 +406,8 @@ MOE_API int moe_check_router(const moe_problem *p, const moe_router *r);
 
 /* logits: device [N][E] of r->logits' type; bias: device float [E] or NULL;
  * topk_ids: int32 [N][k]; topk_weights: float [N][k] or NULL (not computed);
- * scores: float [N][E] for s (a balance loss reads it), or NULL.  One launch. */
+ * scores: float [N][E] for s (a balance loss reads it), or NULL.  Outputs overlap no input
+ * and not each other.  One launch (for every 2^22 tokens). */
 MOE_API int moe_route(const moe_problem *p, const moe_router *r, const void *logits,
                       const float *bias, int32_t *topk_ids, float *topk_weights, float *scores,
                       void *stream);
@@ -422,7 +423,7 @@ MOE_API int moe_route(const moe_problem *p, const moe_router *r, const void *log
  *   otherwise     dlogits = J(dscores + sum_{id_j = e} scale * dweights_j)
  *   J(d)_e = s_e (d_e - sum_f d_f s_f) (softmax), d_e s_e (1 - s_e) (sigmoid)
  * in fp32, rounded once to dlogits [N][E] (r->logits' type), which is written whole.
- * The bias has no gradient: it only orders. */
+ * The bias has no gradient: it only orders.  dlogits overlaps no input. */
 MOE_API int moe_route_backward(const moe_problem *p, const moe_router *r, const void *logits,
                                const int32_t *topk_ids, const float *dweights,
                                const float *dscores, void *dlogits, void *stream);
@@ -553,7 +554,8 @@ MOE_API int moe_expert_linear_backward(const moe_problem *p, const moe_plan *pla
  * is computed from it is NaN and not a finite guess. */
 
 /* x: device bf16 bits [rows][cols], cols % 32 == 0; codes: uint8 [rows][cols/2];
- * scales: uint8 [rows][cols/32].  rows >= 0, rows * cols < 2^46. */
+ * scales: uint8 [rows][cols/32].  rows >= 0, rows * cols < 2^46.  x and codes are 16-byte
+ * aligned; outputs do not overlap x. */
 MOE_API int moe_quantize_mxfp4(int64_t rows, int32_t cols, const uint16_t *x, uint8_t *codes,
                                uint8_t *scales, void *stream);
 
