@@ -232,7 +232,7 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 //   FP8: 16 x 64, K in four 11.2   909.6           92.7         145.6^        690.9
 //        16 x 64            20.2   640.2           78.7         110.7^        520.2
 //        64 x 128           27.6   887.5           69.6          72.7^        225.2
-//        128 x 256          54.1  1406.3          109.8         110.4^        208.4
+//        128 x 256          54.1  1406.3          109.8         110.4^        213.0
 // (* K = 7168, F = 2048, 256 experts; ** linear, K = 2048, N = 4096; *** F = 2048; ^ 32 rows; 96: 133.8
 // of 64 x 128, 114.4 of 128 x 256.)
 // A tile of 16 rows is one wave with two stages, so that a compute unit holds six and the

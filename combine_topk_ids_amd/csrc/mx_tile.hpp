@@ -327,23 +327,22 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
           high[i] = static_cast<int>(v & all);
           low[i] = static_cast<int>(v & ~all);
         }
-        // block b's small codes, then b - 1's large ones, then what b - 2 adds to its sum: no
-        // product waits for the one before it
-        f32x4 d[3];
+        // The product of block b, then what that of b - 1 adds to its sum.  (The halves a block
+        // apart, so that none waits for the other: 435 us for 417, 24576 rows, K = 2048, N = 4096.)
+        f32x4 d[2];
 #pragma unroll
-        for (int b = 0; b < S::FJ + 2; ++b) {
-          if (b < S::FJ)
-            d[b % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+        for (int b = 0; b <= S::FJ; ++b) {
+          if (b < S::FJ) {
+            d[b & 1] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
                 wide(vj[b]), low, f32x4{0.f, 0.f, 0.f, 0.f}, 4, 0, 0, sj[b], 0, 127);
-          if (b >= 1 && b <= S::FJ) {
-            d[(b - 1) % 3] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(vj[b - 1]), high, d[(b - 1) % 3],
-                                                                              4, 0, 0, sj[b - 1], 0, 127);
-            if (last) read_j(b - 1, H ^ 1);
+            d[b & 1] =
+                __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(vj[b]), high, d[b & 1], 4, 0, 0, sj[b], 0, 127);
+            if (last) read_j(b, H ^ 1);
           }
-          if (b >= 2) {
+          if (b > 0) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              acc[a][b - 2][i] = __builtin_fmaf(d[(b - 2) % 3][i], fi[set], acc[a][b - 2][i]);
+              acc[a][b - 1][i] = __builtin_fmaf(d[(b - 1) & 1][i], fi[set], acc[a][b - 1][i]);
           }
         }
       } else {
