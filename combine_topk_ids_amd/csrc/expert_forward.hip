@@ -232,7 +232,7 @@ hipError_t launch(ForwardArgs g, int64_t pairs, int act, hipStream_t stream, int
 // The rows an expert has on average are all the host knows.  Where the routing sends
 // them all to a few experts, the tile picked for few rows is the wrong one (K = 4096,
 // F = 1024, bf16; 64 experts, 768 rows on six of them: K in four 50 us, 64 x 128
-// 25, 128 x 128 42; 256 experts, 3072 rows on six: 182, 69, 54; 6144 rows of 64 experts
+// 25, 128 x 128 42; 256 experts, 512 rows on each of six: 182, 69, 54; 6144 rows of 64 experts
 // on six: 128 x 128 97, 256 x 256 96).
 // FP8 stays with 128 x 128: a 256 x 256 tile's sums, operands and block products
 // do not fit the registers.  With many rows its workgroups take one tile each, so that

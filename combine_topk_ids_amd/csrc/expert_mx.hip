@@ -7,6 +7,12 @@
 // Sums are fp32 accumulators of the scaled matrix instruction (mx_tile.hpp says what it keeps
 // of its terms).  h and y are rounded once: to bf16, or h to MX-FP4 with the scale of
 // its own 32 values, the rows of the next product.
+//
+// Few rows are bound by the weights' bytes (128 tokens, top 8 of 256 experts, K = 7168, F = 2048: 3.93
+// GB in 638 us, 6.2 TB/s), many by the loads to LDS beside the products (8192 tokens of the same
+// layer: 1500 us, 1353 without products, 934 without loads; 2.6 PFLOP/s), FP8 rows by the
+// matrix instructions in two halves and their vector work (24576 rows, K = 2048, N = 4096: 417 us,
+// 346 without loads).
 #include "expert_tile.hpp"
 #include "mx_encode.hpp"
 #include "mx_tile.hpp"

@@ -9,8 +9,12 @@
 // the values' order.  The order of two experts must not hang on a rounding.  Without a bias it is
 // that of the logits, which is exact.  With one, and for sums of two in a group, values are formed
 // in fp32 first; where two that are told apart lie nearer than their errors could
-// move them, the wave forms all of them again in 64 bits (8192 tokens, 256 experts, 8 groups:
-// 64 bits for every token took 29.6 us).
+// move them, the wave forms all of them again in 64 bits (8192 tokens, 256 experts, 8 groups and a
+// bias: 13.5-14.4 us, 64 bits for every token 29.6).
+//
+// Bound by vector instructions (770 a wave of that case) and, for few tokens, by the chain of
+// k + 1 reductions over the lanes: 4.7 us for one token, 6.1 for 16384 of 128 bf16 logits, whose 5 MB
+// are one.
 #include <initializer_list>
 #include <type_traits>
 
@@ -677,6 +681,10 @@ struct RouteGradArgs {
   float scale;
 };
 
+// Softmax: dl = s (d - sum d s); sigmoid: dl = d s (1 - s); renormalised weights w = s / sum s of
+// the chosen: u_j = w_j (d_j - sum d w), times 1 - s_j for a sigmoid.  Read and written once, so
+// bound by the latency of one token's loads: 16384 tokens, 128 experts, bf16, both gradients 6.6 us
+// for 17.8 MB; 333 tokens of 60 3.3.
 template <int L, int PER, class T>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(RouteGradArgs g) {
   constexpr int kTokens = kThreads / L;
