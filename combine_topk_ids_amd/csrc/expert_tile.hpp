@@ -180,7 +180,8 @@ constexpr Operand kNoOperand{nullptr, 0, 0};
 
 // Rows of `row_bytes` stored along c.  ROW(r) maps a tile row to a row of the
 // operand (it must satisfy ROW(a * kLoadRows + b) = ROW(a * kLoadRows) + ROW(b), b < kLoadRows).
-template <class S, int L, class ROW, bool NT = false>
+// PAIRS: chunks 2q and 2q + 1 of a step lie where q and q + 4 would.
+template <class S, int L, class ROW, bool NT = false, bool PAIRS = false>
 struct Along {
   ROW row;
   int row_bytes, chunk;  // chunk: byte offset in a step of what this lane fetches
@@ -189,7 +190,8 @@ struct Along {
   __device__ __forceinline__ void init(int bytes) {
     row_bytes = bytes;
     const int r = group_thread<S>() / 8;
-    chunk = ((group_thread<S>() & 7) ^ (r & 7)) * 16;
+    const int at = (group_thread<S>() & 7) ^ (r & 7);
+    chunk = (PAIRS ? (at & 3) * 2 + (at >> 2) : at) * 16;
     off = row(r) * bytes + chunk;
   }
   __device__ __forceinline__ void issue(lds_ptr to, const Operand &o, int step) const {

@@ -164,8 +164,10 @@ struct Ring {
 
 template <class S, class ROW>
 struct MxFeed {
-  Along<S, S::LI, SameRow> i;
-  Along<S, S::LJ, ROW, S::NT> j;
+  // (MX-FP4 rows: a lane reads chunks 2q and 2q + 1; they lie like the other formats' q and q + 4,
+  // which 16 lanes read without a bank conflict. Side by side, half of the LDS's cycles were conflicts.)
+  Along<S, S::LI, SameRow, false, !S::FP8> i;
+  Along<S, S::LJ, ROW, S::NT, !S::FP8> j;
   PieceLanes<S, ROW> s;
   // step of the contraction that a group takes as its step-th
   __device__ __forceinline__ int global_step(int step) const {
@@ -207,11 +209,10 @@ __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const Mx
   const Wave<S> w = this_wave<S>();
   const int lane = lane_id(), r = lane & 15, q = lane >> 4;
   // places in a stage: of the halves' chunks of row r of the wave's first block
-  const int chunk = S::FP8 ? q : 2 * q;
   const int row_i = w.wi * 16 + r, row_j = w.wj * S::FJ * 16 + r;
-  const int swap = S::FP8 ? 64 : 16;  // between the halves (of an FP8 part: between a lane's chunks)
-  const int at_i = row_i * kStepBytes + ((chunk ^ (r & 7)) * 16);
-  const int at_j = row_j * kStepBytes + ((chunk ^ (r & 7)) * 16);
+  constexpr int swap = 64;  // between the halves (of an FP8 part: between a lane's chunks)
+  const int at_i = row_i * kStepBytes + ((q ^ (r & 7)) * 16);
+  const int at_j = row_j * kStepBytes + ((q ^ (r & 7)) * 16);
   // and, in a piece, of their scales
   int word_i = 0, word_j = 0, scale_i = row_i * S::kRowBytes, scale_j = S::kGroupsI * 1024 + row_j * S::kRowBytes;
   if constexpr (S::FP8) {
