@@ -10,7 +10,7 @@
 //
 // Few rows are bound by the weights' bytes (128 tokens, top 8 of 256 experts, K = 7168, F = 2048: 3.93
 // GB in 638 us, 6.2 TB/s), many by the loads to LDS beside the products (8192 tokens of the same
-// layer: 1500 us, 1353 without products, 934 without loads; 2.6 PFLOP/s), FP8 rows by the
+// layer: 1440 us, 2.7 PFLOP/s; products alone 934), FP8 rows by the
 // matrix instructions in two halves and their vector work (24576 rows, K = 2048, N = 4096: 417 us,
 // 346 without loads).
 #include "expert_tile.hpp"
@@ -231,10 +231,10 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 // 24576 rows, K = 2048, N = 4096, 64 experts 451 us against 390).  Measured, us a call, gated, K = 4096,
 // F = 1024, 64 experts:
 //   rows an expert           0.1     4*     12**   16     24     48    128    192    384***
-//   16 x 64, K in four       8.2   674.6    81.8   65.5   83.1  128.6  304.8  447.5  1738
-//   16 x 64                 15.8   612.0    51.8   63.6   81.3  131.5  311.7  475.0  2068
-//   128 x 128               14.8   680.8    62.2   54.8   55.9   60.5   89.5  103.1   332
-//   256 x 256               21.5   832.3    72.2   65.2   66.1   68.6   80.3   90.6   281
+//   16 x 64, K in four       8.5   600.2    80.2   65.0   82.1  127.6  300.4  441.5  1724
+//   16 x 64                 15.8   613.0    56.0   63.7   80.8  130.9  312.3  475.0  2073
+//   128 x 128               14.7   678.2    61.8   54.8   55.6   60.4   89.5  104.4   329
+//   256 x 256               21.0   829.8    71.4   64.1   65.3   67.8   79.3   90.9   276
 //   FP8: 16 x 64, K in four 11.2   909.6           92.7         145.6^        690.9
 //        16 x 64            20.2   640.2           78.7         110.7^        520.2
 //        64 x 128           27.6   887.5           69.6          72.7^        225.2
@@ -246,10 +246,10 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 // one: 926 us for 640 above).  Where tiles are few the time is that of one chain of steps, and a long
 // contraction goes to the four waves of a workgroup.
 // A short contraction does not pay for 256 x 256's first loads and last stores (256 rows, N = 4096, 128
-// x 128 and 256 x 256: K = 512 59.7 / 61.8, 1024 81.9 / 81.7, 2048 131.0 / 125.8; linear, N = 7168, K = 1024
-// 84.6 / 90.6), nor does one whose rows (K / 2 bytes) start inside a line: of each the two lines
+// x 128 and 256 x 256: K = 512 58.4 / 61.9, 1024 80.6 / 80.8, 2048 130.8 / 124.1; linear, N = 7168, K = 1024
+// 83.2 / 92.1), nor does one whose rows (K / 2 bytes) start inside a line: of each the two lines
 // that a step touches come twice, more often than the caches keep them (256 rows, N = 4096,
-// K = 4128 313 / 579).
+// K = 4128 306 / 460).
 template <bool GLU, bool FP8, bool ODD>
 hipError_t launch_sized(const MxArgs &g, int64_t pairs, hipStream_t stream) {
   typedef MxShape<16, 64, 1, 1, FP8 ? 2 : 3, FP8, ODD, true, 4> Split;
