@@ -136,8 +136,9 @@ __device__ __forceinline__ uint64_t order_key(double v) {
   return pick(v != v, ~uint64_t{0}, pick(v == -__builtin_inf(), uint64_t{0}, key));
 }
 
-// exp to about one unit in the last place (the hardware's exp2 with the argument's
-// rounding put right); zero below 2^-126.
+// exp, off by at most (3 + 0.23 |x|) 2^-24 of itself: the hardware's exp2 (a unit in the last place), a last
+// rounding, and what log2 e loses as an fp32 number (1.93e-8, times |x| ln 2).  The rounding of
+// the argument's product is put right.  Zero below 2^-126.
 __device__ __forceinline__ float exp_fine(float x) {
   constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.693147180559945309417f;
   const float t = x * kLog2e;
@@ -297,11 +298,14 @@ __device__ __forceinline__ double key_value(uint64_t u) {
 
 // Whether fp32 values a >= b could be the other way round, or equal: `slack` is what the errors of
 // two scores (or of two sums of two) can come to, 2^-21 what the additions round.
-// A sigmoid is off by at most 4.2 * 2^-24 (exp_fine's error and that of its argument weigh s (1 - s),
-// the sum and the reciprocal 1.5 * 2^-23 s), four of them by 2^-19.  A softmax score is off by at
-// most 27 * 2^-24 of itself (a sum of 1024 terms, 16 in a lane), and scores of a row add up to 1
-// at most: two sets of them by 2^-18.  (A NaN or two infinities are not near: a score with its bias
-// never overflows, so neither becomes another value in 64 bits.)
+// A sigmoid is off by at most 4.2 * 2^-24 (exp_fine's error weighs s (1 - s), at most 1/4, or 0.224 with
+// the factor |l|; the sum and the reciprocal 1.5 * 2^-23 s), four of them by 2^-19.  A softmax score
+// s = e^x / sum, x = l - top: its exponential is off by (3 + 1.3 |x|) 2^-24 of itself (the
+// rounding of x too), which is at most 3 s + 1.3 / e in all, as s |x| <= 1 / e; the sum by
+// 33 * 2^-24 of itself (its terms' mean |x| is at most log 1024, so 12, and 21 additions),
+// the reciprocal and the product by 2.  Scores of a row add up to 1 at most: four of them by
+// (3 + 35 + 4 * 1.3 / e) 2^-24 = 40 * 2^-24, less than 2^-18.  (A NaN or two infinities are not near: a score
+// with its bias never overflows, so neither becomes another value in 64 bits.)
 constexpr float kSigmoidSlack = 0x1p-19f, kSoftmaxSlack = 0x1p-18f;
 __device__ __forceinline__ bool too_near(float a, float b, float slack) {
   return a - b <= slack + 0x1p-21f * fabsf(a);
