@@ -393,8 +393,8 @@ struct Progress {
 };
 
 // The loads of the first tile's first NST steps.
-template <class S, class F, class Src>
-__device__ __forceinline__ void start(lds_ptr lds, const F &feed, const Src &src) {
+template <class S, class F>
+__device__ __forceinline__ void start(lds_ptr lds, const F &feed, const Source &src) {
 #pragma unroll
   for (int s = 0; s < S::NST; ++s) feed.issue(lds, s, src, s);
 }

@@ -199,9 +199,7 @@ __device__ __forceinline__ void start_mx(lds_ptr lds, const F &feed, const MxSou
   for (int s = 0; s < S::NST; ++s) feed.issue(lds, s, at.loaded, src, s);
 }
 
-// acc[a][b] = the products of cur's steps; as multiply() of expert_tile.hpp.
-// skip_i, skip_j (ODD): what ScaleRows' first byte is past a whole word; blocks: scale blocks
-// of a row.
+// acc[a][b] = the products of cur's steps; as multiply() of expert_tile.hpp.  blocks: scale blocks of a row.
 template <class S, int FI, class F>
 __device__ __forceinline__ void multiply_mx(lds_ptr lds, const F &feed, const MxSource &cur,
                                             const MxSource &next, int blocks, MxProgress &at,
