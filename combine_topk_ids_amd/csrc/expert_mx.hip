@@ -9,10 +9,11 @@
 // its own 32 values, the rows of the next product.
 //
 // Few rows are bound by the weights' bytes (128 tokens, top 8 of 256 experts, K = 7168, F = 2048: 3.93
-// GB in 638 us, 6.2 TB/s), many by the loads to LDS beside the products (8192 tokens of the same
-// layer: 1440 us, 2.7 PFLOP/s; products alone 934), FP8 rows by the
+// GB in 638 us, 6.2 TB/s).  Many rows: a wave's reads of LDS and its products come one after the other
+// (mx_tile.hpp), and the loads to LDS are issued late in a step (8192 tokens of the same layer:
+// 1440-1460 us, 2.7 PFLOP/s, 7.3 GB fetched of 4.2; without loads 934).  FP8 rows: the same, with the
 // matrix instructions in two halves and their vector work (24576 rows, K = 2048, N = 4096: 417 us,
-// 346 without loads).
+// 346 without loads; those 65536 rows of K = 7168 3490-3620).
 #include "expert_tile.hpp"
 #include "mx_encode.hpp"
 #include "mx_tile.hpp"
@@ -250,6 +251,9 @@ hipError_t launch(MxArgs g, int64_t pairs, hipStream_t stream, int resident = S:
 // 83.2 / 92.1), nor does one whose rows (K / 2 bytes) start inside a line: of each the two lines
 // that a step touches come twice, more often than the caches keep them (256 rows, N = 4096,
 // K = 4128 306 / 460).
+// The average is all that the host knows: where a routing sends every row to a few experts, the tile
+// for few rows reads their weights once for every 16 rows (gated, K = 4096, F = 1024, 171 rows on each of
+// six experts: of 256 37 us, with the tile for many rows, which a layer of six gets, 16.6).
 template <bool GLU, bool FP8, bool ODD>
 hipError_t launch_sized(const MxArgs &g, int64_t pairs, hipStream_t stream) {
   typedef MxShape<16, 64, 1, 1, FP8 ? 2 : 3, FP8, ODD, true, 4> Split;

@@ -551,7 +551,9 @@ MOE_API int moe_expert_linear_backward(const moe_problem *p, const moe_plan *pla
  *
  * Encoding is moe_dispatch's (see MOE_FMT_MXFP4_B32), but for a block that holds an
  * infinity or a NaN: it gets the scale byte 255, E8M0's NaN, and zero codes, so that what
- * is computed from it is NaN and not a finite guess. */
+ * is computed from it is NaN and not a finite guess.  This holds for what moe_quantize_mxfp4 and
+ * the gated block encode; moe_dispatch keeps its own rule, under which such a value in a hidden row
+ * becomes a finite code. */
 
 /* x: device bf16 bits [rows][cols], cols % 32 == 0; codes: uint8 [rows][cols/2];
  * scales: uint8 [rows][cols/32].  rows >= 0, rows * cols < 2^46.  x and codes are 16-byte
@@ -574,7 +576,10 @@ MOE_API int moe_check_expert_mx_op(const moe_problem *p, const moe_expert_op *op
  * Products are whole: the scaled matrix instruction keeps every one of MX-FP4 rows, and FP8
  * rows go through it in two halves, codes of 2 and above and codes below, for the same.  It
  * adds them up in fp32 (an addition is off by up to 2^-20 of its largest term); the sums of an
- * FP8 row's blocks are multiplied by its fp32 scale and added in fp32.  Row ranges, untouched
+ * FP8 row's blocks are multiplied by its fp32 scale and added in fp32.  The halves are twice the
+ * matrix work: with few rows, where the weights' bytes count, FP8 rows cost little more than
+ * MX-FP4 rows and half of FP8 weights, with many rows more than either (8192 tokens, top 8 of 256
+ * experts, K = 7168, F = 2048: 3.6 ms; MX-FP4 rows 1.45, FP8 weights 3.1).  Row ranges, untouched
  * rows, repeatability and NaN: as the experts' products above. */
 MOE_API int moe_expert_glu_mx(const moe_problem *p, const moe_plan *plan, const moe_expert_op *op,
                               const void *x, const void *x_scales, const uint8_t *w,
